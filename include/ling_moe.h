@@ -367,6 +367,71 @@ void ling_moe_lmhead_destroy(ling_moe_lmhead_t *h);
  * device-side wait (0 keeps the default, 2 s). */
 int ling_moe_lmhead_test_set_wait(ling_moe_lmhead_t *h, int skip_cta, uint64_t wait_limit_ns);
 
+/* Element types of the calls below. */
+typedef enum { LING_MOE_TYPE_F32 = 0, LING_MOE_TYPE_BF16 = 1 } ling_moe_type_t;
+
+/* ---- beam search ----
+ * What follows the LM head when several continuations of a request are kept:
+ * the selection of the best ones over beams and vocabulary, and the move of
+ * the beams' states to the places of the beams that continue them.  The pages
+ * name no beam search; the definitions are this library's.
+ *
+ * A group (request) has W beams, each with an accumulated score c_w (-inf: a
+ * dead beam, as all but the first are at the first step) and logits z_w.  Its
+ * candidates are, for each token t of a live beam,
+ *   c_w + z_w[t] - log(sum_j exp(z_w[j])),
+ * and for a finished beam the one candidate (eos, c_w).  The W best become the
+ * group's beams, best first; ties go to the lower beam, then (inside a beam
+ * the larger logit, then) the lower token.  Scores are formed in 64 bits and
+ * rounded to fp32 once.  A logit of -inf or NaN is no candidate; a row whose
+ * logits are all that, or hold +inf, has none.  Places that no candidate is
+ * left for get token -1, their own place as parent, score -inf, finished 1. */
+typedef struct ling_moe_beam ling_moe_beam_t; /* opaque handle: the selection's workspace */
+
+/* Allocates the workspace of up to max_groups groups (4.6 KB per beam) on the
+ * current device.  Synchronises the device.  1 <= beams <= 16, 1 <= vocab <= 2^30.
+ * As with every handle, one must not be used by two streams (or two captured
+ * graphs that run at the same time), and its calls belong to its device.
+ * Errors: INVALID_ARG, UNSUPPORTED, OOM, CUDA; *out is then NULL. */
+int ling_moe_beam_create(int max_groups, int beams, int vocab, ling_moe_beam_t **out);
+
+/* Selects on `stream`.  logits: logits_type (fp32 or bf16), element (g, w, t) at
+ * g * group_stride + w * beam_stride + t, any alignment of its element size
+ * (16-byte aligned rows are read faster).  scores fp32 [groups, W]; finished
+ * uint8 [groups, W] (0 or not), or NULL if no beam has finished; eos the token
+ * that finishes a beam, -1 for none (finished must then be NULL).
+ * Outputs, all [groups, W], DEVICE: tokens and parents int32 (parents are
+ * places in the group), scores_out fp32, finished_out uint8 (1 where the token
+ * is eos).  scores_out may be scores and finished_out may be finished (the whole
+ * array); otherwise outputs overlap neither inputs nor one another.
+ * 0 <= groups <= max_groups; 0 enqueues nothing.  One launch; asynchronous, no
+ * allocation, capturable.  Rows of dead and finished beams are not read.
+ * Errors: INVALID_ARG (before anything is enqueued), CUDA. */
+int ling_moe_beam_select(ling_moe_beam_t *h, const void *logits, int logits_type, int64_t group_stride,
+                         int64_t beam_stride, int groups, const float *scores, const uint8_t *finished, int eos,
+                         int32_t *tokens, int32_t *parents, float *scores_out, uint8_t *finished_out, void *stream);
+
+/* Moves the beams' states in place on `stream`: in each of the n_states
+ * tensors (row_bytes[i] bytes per row, num_rows rows, contiguous, DEVICE; the
+ * two arrays are HOST arrays, read during the call) row(g, w) becomes what
+ * row(g, parents[g, w]) was before the call, for all places at once; row(g, w)
+ * is slots[g, w], or g * beams + w where slots is NULL.  parents and slots:
+ * int32 [groups, beams], DEVICE.  A place whose parent is itself is not
+ * touched; neither is one whose parent, slot or parent's slot is out of range.  No two
+ * places may name the same slot (the contents of that row are then
+ * undefined).  Addresses and row sizes that are multiples of 16 move fastest;
+ * any are taken.  One launch per 32 tensors; asynchronous, no allocation, no
+ * workspace, capturable.  1 <= beams <= 16.
+ * Errors: INVALID_ARG (before anything is enqueued), CUDA. */
+int ling_moe_beam_reorder(void *const *states, const size_t *row_bytes, int n_states, int num_rows,
+                          const int32_t *slots, const int32_t *parents, int groups, int beams, void *stream);
+
+/* Number of kernel launches the handle's select calls have enqueued. */
+int64_t ling_moe_beam_launch_count(const ling_moe_beam_t *h);
+
+/* Free the handle.  NULL is a no-op.  No enqueued work may still use it. */
+void ling_moe_beam_destroy(ling_moe_beam_t *h);
+
 #ifdef __cplusplus
 }
 #endif

@@ -23,6 +23,7 @@ __all__ = [
     "ling_moe_kernel_times", "ling_moe_ep_t", "ling_moe_create_ep", "ling_moe_forward_partial",
     "ling_moe_round_bf16", "LING_MOE_FORMAT_INT4", "LING_MOE_FORMAT_MXFP4", "round_bf16",
     "MoELayer", "LMHeadFP8", "EXPORTED",
+    "LING_MOE_TYPE_F32", "LING_MOE_TYPE_BF16", "BeamSearch",
 ]
 
 LING_MOE_OK = 0
@@ -33,6 +34,8 @@ LING_MOE_ERR_UNSUPPORTED = -4
 LING_MOE_ERR_DEVICE_TIMEOUT = -5
 LING_MOE_FORMAT_INT4 = 0
 LING_MOE_FORMAT_MXFP4 = 1
+LING_MOE_TYPE_F32 = 0
+LING_MOE_TYPE_BF16 = 1
 
 # every symbol include/ling_moe.h declares
 EXPORTED = (
@@ -45,6 +48,8 @@ EXPORTED = (
     "ling_moe_lmhead_create", "ling_moe_lmhead_forward", "ling_moe_lmhead_forward_ex",
     "ling_moe_lmhead_forward_host", "ling_moe_lmhead_weights", "ling_moe_lmhead_status",
     "ling_moe_lmhead_launch_count", "ling_moe_lmhead_destroy", "ling_moe_lmhead_test_set_wait",
+    "ling_moe_beam_create", "ling_moe_beam_select", "ling_moe_beam_reorder", "ling_moe_beam_launch_count",
+    "ling_moe_beam_destroy",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -128,6 +133,12 @@ def _load():
         "ling_moe_lmhead_launch_count": (i64, [vp]),
         "ling_moe_lmhead_destroy": (None, [vp]),
         "ling_moe_lmhead_test_set_wait": (ci, [vp, ci, ctypes.c_uint64]),
+        "ling_moe_beam_create": (ci, [ci, ci, ci, ctypes.POINTER(vp)]),
+        "ling_moe_beam_select": (ci, [vp, vp, ci, i64, i64, ci, vp, vp, ci, vp, vp, vp, vp, vp]),
+        "ling_moe_beam_reorder": (ci, [ctypes.POINTER(vp), ctypes.POINTER(ctypes.c_size_t), ci, ci, vp, vp, ci, ci,
+                                       vp]),
+        "ling_moe_beam_launch_count": (i64, [vp]),
+        "ling_moe_beam_destroy": (None, [vp]),
     }
     for name, (res, args) in sig.items():
         try:
@@ -485,3 +496,113 @@ class LMHeadFP8:
             self.close()
         except Exception:
             pass
+
+
+def _raw_stream(torch, stream):
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return getattr(stream, "cuda_stream", stream)
+
+
+def _on_current_device(torch, name, *tensors):
+    """The library launches on the current device: its tensors have to live there."""
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != cur:
+            raise ValueError(f"{name}: a tensor on {t.device}, the current device is cuda:{cur}")
+
+
+class _Handle:
+    """A library handle that is freed with its object."""
+
+    _destroy = None  # name of the C call
+
+    def close(self):
+        if getattr(self, "handle", None):
+            getattr(lib, self._destroy)(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class BeamSearch(_Handle):
+    """Beam search for up to `max_groups` requests of `beams` beams each over `vocab` tokens.
+
+    `select` takes one step's logits (LMHeadFP8's, or any) and the beams'
+    accumulated scores to the next beams; `reorder` moves the beams' states
+    to their new places.  Definitions and limits: ling_moe_beam_select and
+    ling_moe_beam_reorder in ling_moe.h.
+    """
+
+    _destroy = "ling_moe_beam_destroy"
+
+    def __init__(self, max_groups: int, beams: int, vocab: int):
+        import torch  # device memory and streams only
+        self.max_groups, self.beams, self.vocab = int(max_groups), int(beams), int(vocab)
+        h = ctypes.c_void_p()
+        _check(lib.ling_moe_beam_create(self.max_groups, self.beams, self.vocab, ctypes.byref(h)))
+        self.handle = h.value
+        self._torch = torch
+
+    def select(self, logits, scores, finished=None, eos: int = -1, stream=None):
+        """(tokens int32, parents int32, scores fp32, finished bool), each [groups, beams], best first.
+
+        logits: fp32 or bf16 [groups, beams, vocab] or [groups * beams, vocab], the last
+        dimension contiguous; scores fp32 [groups, beams] (-inf: a dead beam); finished
+        bool or uint8 [groups, beams] or None; eos the token that finishes a beam (-1: none)."""
+        torch = self._torch
+        W, V = self.beams, self.vocab
+        if logits.dim() == 2 and logits.shape[0] % W == 0:
+            logits = logits.unflatten(0, (logits.shape[0] // W, W))
+        if (logits.dim() != 3 or tuple(logits.shape[1:]) != (W, V) or not logits.is_cuda
+                or logits.dtype not in (torch.float32, torch.bfloat16) or (V > 1 and logits.stride(2) != 1)):
+            raise ValueError(f"logits must be a CUDA fp32 or bf16 tensor [groups, {W}, {V}] or [groups * {W}, {V}], "
+                             f"contiguous along the vocabulary, got {logits.dtype} {tuple(logits.shape)}")
+        G = logits.shape[0]
+        _require(scores, (G, W), torch.float32, True, "scores")
+        if finished is not None:
+            if finished.dtype not in (torch.bool, torch.uint8):
+                raise ValueError("finished must be bool or uint8")
+            _require(finished, (G, W), finished.dtype, True, "finished")
+        _on_current_device(torch, "select", logits, scores, finished)
+        new = lambda dt: torch.empty((G, W), dtype=dt, device=logits.device)  # noqa: E731
+        tokens, parents, out, done = new(torch.int32), new(torch.int32), new(torch.float32), new(torch.bool)
+        _check(lib.ling_moe_beam_select(
+            self.handle, logits.data_ptr(),
+            LING_MOE_TYPE_F32 if logits.dtype == torch.float32 else LING_MOE_TYPE_BF16, logits.stride(0),
+            logits.stride(1), G, scores.data_ptr(), finished.data_ptr() if finished is not None else None, int(eos),
+            tokens.data_ptr(), parents.data_ptr(), out.data_ptr(), done.data_ptr(), _raw_stream(torch, stream)))
+        return tokens, parents, out, done
+
+    def reorder(self, states, parents, slots=None, stream=None):
+        """In every tensor of `states` (contiguous, [rows, ...]; one tensor or a list of them, all
+        with the same number of rows) the row of beam (g, w) becomes the row that beam
+        (g, parents[g, w]) had; in place.  parents: int32 [groups, beams]; slots: the beams'
+        rows, int32 [groups, beams] (None: row g * beams + w)."""
+        torch = self._torch
+        states = [states] if torch.is_tensor(states) else list(states)
+        if parents.dim() != 2:
+            raise ValueError("parents must be 2-D [groups, beams]")
+        G = parents.shape[0]
+        _require(parents, (G, self.beams), torch.int32, True, "parents")
+        if slots is not None:
+            _require(slots, (G, self.beams), torch.int32, True, "slots")
+        _on_current_device(torch, "reorder", parents, slots, *states)
+        if not states:
+            return
+        rows = states[0].shape[0] if states[0].dim() else 0
+        for t in states:
+            if t.dim() < 1 or t.shape[0] != rows or not t.is_contiguous():
+                raise ValueError("states must be contiguous CUDA tensors with the same number of rows")
+        n = len(states)
+        ptr = (ctypes.c_void_p * n)(*[t.data_ptr() for t in states])
+        nb = (ctypes.c_size_t * n)(*[(t.numel() // rows if rows else 0) * t.element_size() for t in states])
+        _check(lib.ling_moe_beam_reorder(ptr, nb, n, rows, slots.data_ptr() if slots is not None else None,
+                                         parents.data_ptr(), G, self.beams, _raw_stream(torch, stream)))
+
+    def launch_count(self) -> int:
+        return lib.ling_moe_beam_launch_count(self.handle)
