@@ -370,6 +370,59 @@ int ling_moe_lmhead_test_set_wait(ling_moe_lmhead_t *h, int skip_cta, uint64_t w
 /* Element types of the calls below. */
 typedef enum { LING_MOE_TYPE_F32 = 0, LING_MOE_TYPE_BF16 = 1 } ling_moe_type_t;
 
+/* ---- block-FP8 linear layer ----
+ * The projections around the MoE layer, in the block-FP8 form of the model's
+ * checkpoints (vLLM recipe page "inclusionAI/Ling-3.0-flash", section Overview;
+ * the page does not define the format, this library takes the following).
+ *   weights: e4m3 codes [out_features, in_features] row-major, one fp32 scale per
+ *         block of 128 outputs x 128 inputs, [ceil(out / 128), ceil(in / 128)]
+ *         row-major, w = code * scale;
+ *   tokens: quantised at every call, one fp32 scale per token and 128 inputs,
+ *         s_x = max|x| * (1 / 448) (1 for zeros), codes e4m3(x / s_x) to nearest
+ *         even, saturating; 1 / 448, the product and the division each rounded
+ *         once to fp32;
+ *   out[t, n] = sum over the blocks b of 128 inputs of
+ *         s_x[t, b] * s_w[n / 128, b] * (sum_k x_code[t, k] * w_code[n, k]),
+ *         products exact, sums in fp32, one rounding to the output type.
+ * A non-finite x spoils its own token's outputs only. */
+typedef struct ling_moe_fp8_linear ling_moe_fp8_linear_t; /* opaque handle */
+
+/* Copies the weights (DEVICE; codes any alignment, scales 4-byte aligned; free
+ * afterwards) into library memory padded to blocks of 128, with a workspace for
+ * max_tokens quantised tokens.  Synchronises the device.
+ * Limits: 1 <= out_features, max_tokens <= 2^24, 1 <= in_features <= 2^22.
+ * Errors: INVALID_ARG, UNSUPPORTED, OOM, CUDA; *out is then NULL. */
+int ling_moe_fp8_linear_create(const uint8_t *codes, const float *scales, int out_features, int in_features,
+                               int max_tokens, ling_moe_fp8_linear_t **out);
+
+/* out[T, out_features] (out_type fp32 or bf16) of the tokens x[T, in_features]
+ * (bf16) on `stream`; rows x_stride and out_stride elements apart (at least a
+ * row; not read for T <= 1), elements of a row contiguous, any alignment of the
+ * element size (16-byte aligned rows are faster).  out must not overlap x.
+ * 0 <= T <= max_tokens; T == 0 enqueues nothing.  Two launches (quantisation;
+ * product: up to 8 tokens a weight-streaming kernel, more the tensor-core
+ * tiles); asynchronous, no allocation, capturable.  Device-side failures (a
+ * bounded wait that gave up) are reported by ling_moe_fp8_linear_status.
+ * Errors: INVALID_ARG (before anything is enqueued), CUDA. */
+int ling_moe_fp8_linear_forward(ling_moe_fp8_linear_t *h, const void *x, int64_t x_stride, int T, void *out,
+                                int out_type, int64_t out_stride, void *stream);
+
+/* Synchronise `stream` and return the handle's sticky device error: OK, or
+ * DEVICE_TIMEOUT (the word is cleared), or CUDA. */
+int ling_moe_fp8_linear_status(ling_moe_fp8_linear_t *h, void *stream);
+
+/* Number of kernel launches the handle's forward calls have enqueued. */
+int64_t ling_moe_fp8_linear_launch_count(const ling_moe_fp8_linear_t *h);
+
+/* Free the handle.  NULL is a no-op.  No enqueued work may still use it. */
+void ling_moe_fp8_linear_destroy(ling_moe_fp8_linear_t *h);
+
+/* Test hook: skip_cta >= 0 makes that CTA of the next tensor-core launches issue
+ * none of its loads, so that its waits run out and the launch ends with an
+ * error status instead of hanging; -1 turns it off.  wait_limit_ns bounds the
+ * device-side waits (0: the default, 2 s). */
+int ling_moe_fp8_linear_test_set_wait(ling_moe_fp8_linear_t *h, int skip_cta, uint64_t wait_limit_ns);
+
 /* ---- beam search ----
  * What follows the LM head when several continuations of a request are kept:
  * the selection of the best ones over beams and vocabulary, and the move of

@@ -23,7 +23,7 @@ __all__ = [
     "ling_moe_kernel_times", "ling_moe_ep_t", "ling_moe_create_ep", "ling_moe_forward_partial",
     "ling_moe_round_bf16", "LING_MOE_FORMAT_INT4", "LING_MOE_FORMAT_MXFP4", "round_bf16",
     "MoELayer", "LMHeadFP8", "EXPORTED",
-    "LING_MOE_TYPE_F32", "LING_MOE_TYPE_BF16", "BeamSearch",
+    "LING_MOE_TYPE_F32", "LING_MOE_TYPE_BF16", "BeamSearch", "BlockFP8Linear",
 ]
 
 LING_MOE_OK = 0
@@ -50,6 +50,8 @@ EXPORTED = (
     "ling_moe_lmhead_launch_count", "ling_moe_lmhead_destroy", "ling_moe_lmhead_test_set_wait",
     "ling_moe_beam_create", "ling_moe_beam_select", "ling_moe_beam_reorder", "ling_moe_beam_launch_count",
     "ling_moe_beam_destroy",
+    "ling_moe_fp8_linear_create", "ling_moe_fp8_linear_forward", "ling_moe_fp8_linear_status",
+    "ling_moe_fp8_linear_launch_count", "ling_moe_fp8_linear_destroy", "ling_moe_fp8_linear_test_set_wait",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -139,6 +141,12 @@ def _load():
                                        vp]),
         "ling_moe_beam_launch_count": (i64, [vp]),
         "ling_moe_beam_destroy": (None, [vp]),
+        "ling_moe_fp8_linear_create": (ci, [vp, vp, ci, ci, ci, ctypes.POINTER(vp)]),
+        "ling_moe_fp8_linear_forward": (ci, [vp, vp, i64, ci, vp, ci, i64, vp]),
+        "ling_moe_fp8_linear_status": (ci, [vp, vp]),
+        "ling_moe_fp8_linear_launch_count": (i64, [vp]),
+        "ling_moe_fp8_linear_destroy": (None, [vp]),
+        "ling_moe_fp8_linear_test_set_wait": (ci, [vp, ci, ctypes.c_uint64]),
     }
     for name, (res, args) in sig.items():
         try:
@@ -606,3 +614,67 @@ class BeamSearch(_Handle):
 
     def launch_count(self) -> int:
         return lib.ling_moe_beam_launch_count(self.handle)
+
+
+class BlockFP8Linear(_Handle):
+    """y = x W^T with e4m3 weights that carry one fp32 scale per 128 x 128 block.
+
+    codes: [out_features, in_features], torch.float8_e4m3fn or its bytes as uint8;
+    scales: fp32 [ceil(out / 128), ceil(in / 128)]; contiguous CUDA tensors, copied.
+    Tokens are bf16 and are quantised per call (one scale per token and 128 inputs).
+    The arithmetic is defined at ling_moe_fp8_linear_forward in ling_moe.h."""
+
+    _destroy = "ling_moe_fp8_linear_destroy"
+
+    def __init__(self, codes, scales, max_tokens: int):
+        import torch  # device memory and streams only
+        if codes.dim() != 2 or codes.dtype not in (torch.float8_e4m3fn, torch.uint8):
+            raise ValueError("codes must be 2-D float8_e4m3fn or uint8")
+        self.out_features, self.in_features = codes.shape
+        self.max_tokens = int(max_tokens)
+        _require(codes, tuple(codes.shape), codes.dtype, True, "codes")
+        _require(scales, (-(-codes.shape[0] // 128), -(-codes.shape[1] // 128)), torch.float32, True, "scales")
+        _on_current_device(torch, "BlockFP8Linear", codes, scales)
+        # the library copies on the legacy default stream: what the caller's stream still writes has to be there
+        torch.cuda.current_stream().synchronize()
+        h = ctypes.c_void_p()
+        _check(lib.ling_moe_fp8_linear_create(codes.data_ptr(), scales.data_ptr(), self.out_features,
+                                              self.in_features, self.max_tokens, ctypes.byref(h)))
+        self.handle = h.value
+        self._torch = torch
+
+    def forward(self, x, out=None, out_dtype=None, stream=None):
+        """[T, out_features] of x [T, in_features] (bf16; rows may be strided).  out_dtype: bf16
+        (default) or fp32; out: a tensor to write, rows may be strided."""
+        torch = self._torch
+        N, K = self.out_features, self.in_features
+        if (x.dim() != 2 or x.shape[1] != K or x.dtype != torch.bfloat16 or not x.is_cuda
+                or (K > 1 and x.stride(1) != 1)):
+            raise ValueError(f"x must be a CUDA bf16 tensor [T, {K}] with contiguous rows, got {x.dtype} "
+                             f"{tuple(x.shape)} on {x.device}")
+        T = x.shape[0]
+        if out is None:
+            out = torch.empty((T, N), dtype=out_dtype or torch.bfloat16, device=x.device)
+        if (tuple(out.shape) != (T, N) or out.dtype not in (torch.bfloat16, torch.float32)
+                or out.dtype != (out_dtype or out.dtype) or not out.is_cuda or (N > 1 and out.stride(1) != 1)):
+            raise ValueError(f"out must be a CUDA bf16 or fp32 tensor [{T}, {N}] with contiguous rows, got {out.dtype} "
+                             f"{tuple(out.shape)} on {out.device}")
+        _on_current_device(torch, "forward", x, out)
+        _check(lib.ling_moe_fp8_linear_forward(
+            self.handle, x.data_ptr(), x.stride(0), T, out.data_ptr(),
+            LING_MOE_TYPE_BF16 if out.dtype == torch.bfloat16 else LING_MOE_TYPE_F32, out.stride(0),
+            _raw_stream(torch, stream)))
+        return out
+
+    __call__ = forward
+
+    def status(self, stream=None) -> int:
+        """Status code of the handle's device work (does not raise on DEVICE_TIMEOUT)."""
+        return lib.ling_moe_fp8_linear_status(self.handle, _raw_stream(self._torch, stream))
+
+    def launch_count(self) -> int:
+        return lib.ling_moe_fp8_linear_launch_count(self.handle)
+
+    def test_set_wait(self, skip_cta: int, wait_limit_ns: int = 0):
+        """Test hook (see ling_moe_fp8_linear_test_set_wait)."""
+        _check(lib.ling_moe_fp8_linear_test_set_wait(self.handle, skip_cta, wait_limit_ns))

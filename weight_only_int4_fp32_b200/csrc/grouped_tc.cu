@@ -31,6 +31,7 @@
 // Ling-3.0-flash MoE inferenciajanak" ("Modell es kiindulo konfiguracio").
 #include "common.cuh"
 #include "grouped_tc.h"
+#include "tcgen05.cuh"
 
 namespace lingmoe {
 
@@ -64,7 +65,6 @@ constexpr int kTmemCols = 512;                  // 2 buffers x (2 M-halves x 128
 // two 4-byte (row pair) words of the stage's two groups.
 constexpr int kRawCodes = 4 * kProd * 8;
 constexpr int kRawStage = kRawCodes + kProd * 8;  // 10 KB
-constexpr unsigned long long kTcWaitNs = 2000000000ull;
 
 __host__ __device__ constexpr int tc_bparts(int mode) { return mode == 0 ? 1 : 2; }
 // down's code ring depth; gate/up loads its codes straight into registers
@@ -84,43 +84,7 @@ static_assert(tc_smem(1) <= 232448, "down-projection pipeline exceeds 227 KB of 
 static_assert(tc_smem(0) <= 232448, "gate/up pipeline exceeds 227 KB of shared memory");
 
 
-// ---------------------------------------------------------------- PTX helpers
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
-  // K-major, 128B swizzle: 8-row atoms of 128 B, atoms 1024 B apart (SBO),
-  // LBO unused (1), descriptor version 1, layout type 2.
-  return (uint64_t)((saddr >> 4) & 0x3FFFu) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-}
-__device__ __forceinline__ uint32_t make_idesc(int n) {
-  // D = f32, A = B = f16, both K-major, M = 128, N = n
-  return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
-}
-__device__ __forceinline__ void tc_mma(uint32_t tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %6, %7, %8}, p;\n\t}"
-      :: "r"(tmem), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(0), "r"(0), "r"(0), "r"(0));
-}
-__device__ __forceinline__ void tc_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-               :: "r"(smem_u32(bar)) : "memory");
-}
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared.b64 _, [%0];" :: "r"(smem_u32(bar)) : "memory");
-}
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float v[16]) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
+// ---------------------------------------------------------------- PTX helpers (the shared ones: tcgen05.cuh)
 __device__ __forceinline__ void tmem_ld16x2(uint32_t ta, uint32_t tb, float va[16], float vb[16]) {
   uint32_t r[16], q[16];
   asm volatile(
@@ -145,28 +109,6 @@ __device__ __forceinline__ void tmem_ld16x2(uint32_t ta, uint32_t tb, float va[1
 __device__ __forceinline__ float tc_silu_mul_scaled(float g, float u, float s) {
   return __fdividef(g, 1.0f + __expf(-(g * s))) * u;
 }
-// 2-D tiled TMA load (no multicast) into this CTA's shared memory.
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-      :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar)) : "memory");
-}
-
-// bounded wait used by every role; on time-out sets the error word and the
-// CTA's abort flag and returns false
-__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, unsigned int* err, int* abort) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const unsigned long long t0 = globaltimer_ns();
-  while (!mbar_try_wait(bar, parity)) {
-    if (*reinterpret_cast<volatile int*>(abort) || globaltimer_ns() - t0 > kTcWaitNs) {
-      atomicOr(err, 4u);
-      *reinterpret_cast<volatile int*>(abort) = 1;
-      return false;
-    }
-  }
-  return true;
-}
-
 // ---------------------------------------------------------------- dequantisation
 // Two exact fp16 weights from a nibble pair (1024 + n in each half):
 // v - 1032 = q is exact, and so is q * s' for s' = s * 2^8 (q has at most 4
@@ -720,38 +662,9 @@ cudaError_t setup_grouped_tc() {
   return e != cudaSuccess ? e : setup_c<kCodecMxfp4>();
 }
 
-namespace {
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return reinterpret_cast<EncodeTiledFn>(f);
-  }();
-  return fn;
+static cudaError_t encode_2d(CUtensorMap* m, const __half* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
+  return tma_encode_2d(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, sizeof(__half), base, rows, cols, 64, box_rows);
 }
-
-// fp16 matrix [rows, cols] row-major; boxes of 64 columns (128 B) x box_rows,
-// 128-byte swizzle, zero fill outside the matrix
-cudaError_t encode_2d(CUtensorMap* m, const __half* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return cudaErrorNotSupported;
-  const cuuint64_t dims[2] = {cols, rows};
-  const cuuint64_t strides[1] = {cols * sizeof(__half)};
-  const cuuint32_t box[2] = {64, box_rows};
-  const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<__half*>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-}  // namespace
 
 cudaError_t tc_encode_maps(TcMaps* m, const __half* xg, const __half* h16, int rows, const __half* shgu16,
                            const __half* shdn16) {
