@@ -423,6 +423,99 @@ void ling_moe_fp8_linear_destroy(ling_moe_fp8_linear_t *h);
  * device-side waits (0: the default, 2 s). */
 int ling_moe_fp8_linear_test_set_wait(ling_moe_fp8_linear_t *h, int skip_cta, uint64_t wait_limit_ns);
 
+/* ---- gated delta rule ----
+ * The recurrence of the model's linear-attention layers (bpdata article,
+ * section "Modell es kiindulo konfiguracio": 35 KDA layers; the pages give no
+ * formula, the definition is this library's).  A sequence holds one fp32 state
+ * S [head_k, head_v] per value head.  Each of its tokens, with query and key of
+ * the key head j / (v_heads / k_heads) of value head j, both divided by
+ * sqrt(sum of squares + 1e-6), a log-decay g <= 0 (per channel of the key, or
+ * one per head), a write strength beta and a value v:
+ *   S <- diag(exp(g)) S
+ *   u  = beta (v - S^T k)
+ *   S <- S + k u^T
+ *   out = scale * S^T q                                        -> bf16
+ * g > 0 counts as 0; -inf forgets everything.  0 <= beta <= 2 (beyond that the
+ * recurrence itself may grow without bound and a prefill's terms may overflow).
+ * States are held and returned in fp32: the step computes in fp32, a prefill
+ * takes two fp16 terms of each operand that feeds the state (about 22 bits);
+ * operands that feed only the bf16 output take one.  Non-finite inputs spoil their own
+ * sequence and head only. */
+typedef struct {
+  int k_heads, v_heads;  /* v_heads a multiple of k_heads */
+  int head_k, head_v;    /* 64 or 128 each */
+  int max_tokens;        /* of a prefill call, all sequences together */
+  int max_seqs;          /* sequences of a call */
+  float scale;           /* of the output; 0: 1 / sqrt(head_k) */
+} ling_moe_delta_config_t;
+
+/* The tensors of a call, all DEVICE.  Strides in elements, none negative:
+ * [0] from sequence to sequence (step only), [1] from token to token, [2] from
+ * head to head; the last dimension of q, k and v is contiguous.  Any alignment
+ * of the element size is taken; 8-byte aligned rows of q and k and 16-byte
+ * aligned rows of g are read faster. */
+typedef struct {
+  const void *q, *k, *v;      /* bf16: k_heads x head_k, k_heads x head_k, v_heads x head_v per token */
+  const float *g;             /* fp32: v_heads x head_k (g_channel_stride 1) or v_heads (0) per token */
+  const float *beta;          /* fp32: v_heads per token */
+  int64_t q_stride[3], k_stride[3], v_stride[3], g_stride[3], beta_stride[3];
+  int64_t g_channel_stride;
+  void *out;                  /* bf16, contiguous [..., v_heads, head_v], 16-byte aligned */
+  float *state;               /* fp32 [num_slots, v_heads, head_k, head_v], contiguous, 16-byte aligned, updated in place */
+  int num_slots;
+  const int32_t *slots;       /* int32 [sequences]: each sequence's row of state; NULL: its own number.  A slot
+                               * outside [0, num_slots) marks padding: that sequence's out rows and all states stay as
+                               * they were.  No two sequences of a call may share a slot (its state is then undefined). */
+} ling_moe_delta_io_t;
+
+typedef struct ling_moe_delta ling_moe_delta_t; /* opaque handle: the prefill's workspace */
+
+/* Checks cfg and allocates the workspace on the current device (at most about
+ * 640 records of 107 KB, one per 64 tokens and head, or one record per head where there
+ * are more heads).  Synchronises the device.  As with every handle, one must
+ * not be used by two streams (or two captured graphs that run at the same
+ * time), and its calls belong to its device.
+ * Errors: INVALID_ARG, UNSUPPORTED, OOM, CUDA; *out is then NULL. */
+int ling_moe_delta_create(const ling_moe_delta_config_t *cfg, ling_moe_delta_t **out);
+
+/* The next `tokens` (0..8) tokens of each of `seqs` sequences, [seqs, tokens, ...]:
+ * a decode step (1) or a verify window.  accepted: int32 [seqs] (DEVICE) or NULL:
+ * the state advances by only the first accepted[i] tokens (clamped to [0,
+ * tokens]; 0: not at all) while out is given for all of them, so a window can be
+ * run before it is known how much of it stands, and its accepted part run
+ * again.  NULL: all.  One launch; asynchronous, no allocation, capturable.
+ * Errors: INVALID_ARG (before anything is enqueued), CUDA. */
+int ling_moe_delta_step(ling_moe_delta_t *h, const ling_moe_delta_io_t *io, int seqs, int tokens,
+                        const int32_t *accepted, void *stream);
+
+/* Packed prompts: sequence i is tokens [cu_seqlens[i], cu_seqlens[i + 1]) of the
+ * call's [tokens, ...] tensors (int32 [seqs + 1], DEVICE, ascending from 0; values
+ * outside [0, tokens] or descending are clamped).  A sequence may be empty (its
+ * state stays as it is) and rows behind the last one are left as they were.
+ * fresh: uint8 [seqs] (DEVICE) or NULL: sequences that start from a zero state
+ * whatever their slot holds.  Chunks of 64 tokens; two launches per segment of
+ * chunks that the workspace holds.  Asynchronous, no allocation, capturable.
+ * Device-side failures (a bounded wait that gave up) are reported by
+ * ling_moe_delta_status.  Errors: INVALID_ARG (before anything is enqueued), CUDA. */
+int ling_moe_delta_prefill(ling_moe_delta_t *h, const ling_moe_delta_io_t *io, int tokens, const int32_t *cu_seqlens,
+                           int seqs, const uint8_t *fresh, void *stream);
+
+/* Synchronise `stream` and return the handle's sticky device error: OK, or
+ * DEVICE_TIMEOUT (the word is cleared), or CUDA. */
+int ling_moe_delta_status(ling_moe_delta_t *h, void *stream);
+
+/* Number of kernel launches the handle's calls have enqueued. */
+int64_t ling_moe_delta_launch_count(const ling_moe_delta_t *h);
+
+/* Free the handle.  NULL is a no-op.  No enqueued work may still use it. */
+void ling_moe_delta_destroy(ling_moe_delta_t *h);
+
+/* Test hook: with skip != 0 the next prefills issue none of their copies, so
+ * that their waits run out and the launches end with an error status instead of
+ * hanging (states and outputs of such a call are void).  wait_limit_ns bounds
+ * the device-side waits (0: the default, 2 s). */
+int ling_moe_delta_test_set_wait(ling_moe_delta_t *h, int skip, uint64_t wait_limit_ns);
+
 /* ---- beam search ----
  * What follows the LM head when several continuations of a request are kept:
  * the selection of the best ones over beams and vocabulary, and the move of

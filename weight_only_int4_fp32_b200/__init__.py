@@ -24,6 +24,7 @@ __all__ = [
     "ling_moe_round_bf16", "LING_MOE_FORMAT_INT4", "LING_MOE_FORMAT_MXFP4", "round_bf16",
     "MoELayer", "LMHeadFP8", "EXPORTED",
     "LING_MOE_TYPE_F32", "LING_MOE_TYPE_BF16", "BeamSearch", "BlockFP8Linear",
+    "GatedDeltaRule", "ling_moe_delta_config_t", "ling_moe_delta_io_t",
 ]
 
 LING_MOE_OK = 0
@@ -52,6 +53,8 @@ EXPORTED = (
     "ling_moe_beam_destroy",
     "ling_moe_fp8_linear_create", "ling_moe_fp8_linear_forward", "ling_moe_fp8_linear_status",
     "ling_moe_fp8_linear_launch_count", "ling_moe_fp8_linear_destroy", "ling_moe_fp8_linear_test_set_wait",
+    "ling_moe_delta_create", "ling_moe_delta_step", "ling_moe_delta_prefill", "ling_moe_delta_status",
+    "ling_moe_delta_launch_count", "ling_moe_delta_destroy", "ling_moe_delta_test_set_wait",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -81,6 +84,19 @@ class ling_moe_weights_t(ctypes.Structure):
 class ling_moe_ep_t(ctypes.Structure):
     _fields_ = [("expert_begin", ctypes.c_int), ("expert_count", ctypes.c_int), ("with_shared", ctypes.c_int),
                 ("format", ctypes.c_int)]
+
+
+class ling_moe_delta_config_t(ctypes.Structure):
+    _fields_ = [("k_heads", ctypes.c_int), ("v_heads", ctypes.c_int), ("head_k", ctypes.c_int),
+                ("head_v", ctypes.c_int), ("max_tokens", ctypes.c_int), ("max_seqs", ctypes.c_int),
+                ("scale", ctypes.c_float)]
+
+
+class ling_moe_delta_io_t(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "v", "g", "beta")]
+                + [(n + "_stride", ctypes.c_int64 * 3) for n in ("q", "k", "v", "g", "beta")]
+                + [("g_channel_stride", ctypes.c_int64), ("out", ctypes.c_void_p), ("state", ctypes.c_void_p),
+                   ("num_slots", ctypes.c_int), ("slots", ctypes.c_void_p)])
 
 
 _LIB = None
@@ -141,6 +157,13 @@ def _load():
                                        vp]),
         "ling_moe_beam_launch_count": (i64, [vp]),
         "ling_moe_beam_destroy": (None, [vp]),
+        "ling_moe_delta_create": (ci, [ctypes.POINTER(ling_moe_delta_config_t), ctypes.POINTER(vp)]),
+        "ling_moe_delta_step": (ci, [vp, ctypes.POINTER(ling_moe_delta_io_t), ci, ci, vp, vp]),
+        "ling_moe_delta_prefill": (ci, [vp, ctypes.POINTER(ling_moe_delta_io_t), ci, vp, ci, vp, vp]),
+        "ling_moe_delta_status": (ci, [vp, vp]),
+        "ling_moe_delta_launch_count": (i64, [vp]),
+        "ling_moe_delta_destroy": (None, [vp]),
+        "ling_moe_delta_test_set_wait": (ci, [vp, ci, ctypes.c_uint64]),
         "ling_moe_fp8_linear_create": (ci, [vp, vp, ci, ci, ci, ctypes.POINTER(vp)]),
         "ling_moe_fp8_linear_forward": (ci, [vp, vp, i64, ci, vp, ci, i64, vp]),
         "ling_moe_fp8_linear_status": (ci, [vp, vp]),
@@ -678,3 +701,115 @@ class BlockFP8Linear(_Handle):
     def test_set_wait(self, skip_cta: int, wait_limit_ns: int = 0):
         """Test hook (see ling_moe_fp8_linear_test_set_wait)."""
         _check(lib.ling_moe_fp8_linear_test_set_wait(self.handle, skip_cta, wait_limit_ns))
+
+
+class GatedDeltaRule(_Handle):
+    """The gated delta rule of the linear-attention layers (definition: ling_moe.h).
+
+    Per value head a fp32 state [head_k, head_v] in a pool [slots, v_heads, head_k, head_v]
+    that `step` (decode and verify windows) and `prefill` (packed prompts) update in place.
+    q and k are normalised inside; g are log-decays (<= 0), per channel [..., v_heads, head_k]
+    or per head [..., v_heads]; beta are the write strengths.  scale: of the output
+    (None: head_k ** -0.5)."""
+
+    _destroy = "ling_moe_delta_destroy"
+    MAX_STEP = 8
+
+    def __init__(self, k_heads: int, v_heads: int, head_k: int, head_v: int, max_tokens: int, max_seqs: int,
+                 scale: float | None = None):
+        import torch  # device memory and streams only
+        self.k_heads, self.v_heads, self.head_k, self.head_v = int(k_heads), int(v_heads), int(head_k), int(head_v)
+        self.max_tokens, self.max_seqs = int(max_tokens), int(max_seqs)
+        if scale is not None and float(scale) == 0.0:
+            raise ValueError("scale must not be 0")
+        cfg = ling_moe_delta_config_t(self.k_heads, self.v_heads, self.head_k, self.head_v, self.max_tokens,
+                                      self.max_seqs, 0.0 if scale is None else float(scale))
+        h = ctypes.c_void_p()
+        _check(lib.ling_moe_delta_create(ctypes.byref(cfg), ctypes.byref(h)))
+        self.handle = h.value
+        self._torch = torch
+
+    def _io(self, lead, q, k, v, g, beta, state, slots, seqs, out):
+        """Check the tensors of a call with leading dimensions `lead` and fill its ling_moe_delta_io_t."""
+        torch = self._torch
+        Hk, Hv, dk, dv = self.k_heads, self.v_heads, self.head_k, self.head_v
+        nl = len(lead)
+        gc = 1 if g.dim() == nl + 2 else 0
+        for name, t, tail, dt in (("q", q, (Hk, dk), torch.bfloat16), ("k", k, (Hk, dk), torch.bfloat16),
+                                  ("v", v, (Hv, dv), torch.bfloat16), ("g", g, (Hv, dk) if gc else (Hv,), torch.float32),
+                                  ("beta", beta, (Hv,), torch.float32)):
+            if t.shape != lead + tail or t.dtype != dt or not t.is_cuda:
+                raise ValueError(f"{name} must be a CUDA {dt} tensor of shape {tuple(lead + tail)}, got {t.dtype} "
+                                 f"{tuple(t.shape)} on {t.device}")
+        for name, t in (("q", q), ("k", k), ("v", v)):
+            if t.stride(-1) != 1:
+                raise ValueError(f"{name} must be contiguous along its last dimension")
+        if gc and g.stride(-1) not in (0, 1):
+            raise ValueError("g must be contiguous (or expanded) along its last dimension")
+        if (state.dim() != 4 or state.shape[1:] != (Hv, dk, dv) or state.dtype != torch.float32 or not state.is_cuda
+                or not state.is_contiguous()):
+            raise ValueError(f"state must be a contiguous CUDA float32 tensor [slots, {Hv}, {dk}, {dv}], got {state.dtype} "
+                             f"{tuple(state.shape)} on {state.device}")
+        if slots is not None:
+            _require(slots, (seqs,), torch.int32, True, "slots")
+        if out is None:
+            out = torch.empty(lead + (Hv, dv), dtype=torch.bfloat16, device=q.device)
+        else:
+            _require(out, lead + (Hv, dv), torch.bfloat16, True, "out")
+        _on_current_device(torch, "delta rule", q, k, v, g, beta, state, slots, out)
+        st = lambda t: tuple(t.stride()[:3]) if nl == 2 else (0, t.stride(0), t.stride(1))  # noqa: E731
+        io = ling_moe_delta_io_t(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), st(q), st(k),
+                                 st(v), st(g), st(beta), g.stride(-1) if gc else 0, out.data_ptr(), state.data_ptr(),
+                                 state.shape[0], slots.data_ptr() if slots is not None else None)
+        return io, out
+
+    def step(self, q, k, v, g, beta, state, slots=None, accepted=None, out=None, stream=None):
+        """out bf16 [B, n, v_heads, head_v] of the next n (<= 8) tokens of B sequences: q, k
+        [B, n, k_heads, head_k], v [B, n, v_heads, head_v], g, beta [B, n, v_heads(, head_k)].
+        slots: int32 [B], the sequences' rows of `state` (None: 0..B-1; outside the pool: padding,
+        left untouched); accepted: int32 [B], how many tokens each state advances by (None: all)."""
+        torch = self._torch
+        if q.dim() != 4:
+            raise ValueError("q must be 4-D [sequences, tokens, heads, head_k]")
+        B, n = q.shape[:2]
+        io, out = self._io(q.shape[:2], q, k, v, g, beta, state, slots, B, out)
+        if accepted is not None:
+            _require(accepted, (B,), torch.int32, True, "accepted")
+            _on_current_device(torch, "step", accepted)
+        _check(lib.ling_moe_delta_step(self.handle, ctypes.byref(io), B, n,
+                                       accepted.data_ptr() if accepted is not None else None,
+                                       _raw_stream(torch, stream)))
+        return out
+
+    def prefill(self, q, k, v, g, beta, state, cu_seqlens, slots=None, fresh=None, out=None, stream=None):
+        """out bf16 [T, v_heads, head_v] of packed sequences: tokens cu_seqlens[i] .. cu_seqlens[i + 1]
+        (int32 [S + 1], on the GPU) are sequence i.  fresh: bool or uint8 [S], sequences that start
+        from a zero state (None: all start from their slot's)."""
+        torch = self._torch
+        if q.dim() != 3:
+            raise ValueError("q must be 3-D [tokens, heads, head_k]")
+        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+            raise ValueError("cu_seqlens must be 1-D [sequences + 1]")
+        S = cu_seqlens.shape[0] - 1
+        _require(cu_seqlens, (S + 1,), torch.int32, True, "cu_seqlens")
+        if fresh is not None:
+            if fresh.dtype not in (torch.bool, torch.uint8):
+                raise ValueError("fresh must be bool or uint8")
+            _require(fresh, (S,), fresh.dtype, True, "fresh")
+        io, out = self._io(q.shape[:1], q, k, v, g, beta, state, slots, S, out)
+        _on_current_device(torch, "prefill", cu_seqlens, fresh)
+        _check(lib.ling_moe_delta_prefill(self.handle, ctypes.byref(io), q.shape[0], cu_seqlens.data_ptr(), S,
+                                          fresh.data_ptr() if fresh is not None else None,
+                                          _raw_stream(torch, stream)))
+        return out
+
+    def status(self, stream=None) -> int:
+        """Status code of the handle's device work (does not raise on DEVICE_TIMEOUT)."""
+        return lib.ling_moe_delta_status(self.handle, _raw_stream(self._torch, stream))
+
+    def launch_count(self) -> int:
+        return lib.ling_moe_delta_launch_count(self.handle)
+
+    def test_set_wait(self, skip: bool, wait_limit_ns: int = 0):
+        """Test hook (see ling_moe_delta_test_set_wait)."""
+        _check(lib.ling_moe_delta_test_set_wait(self.handle, int(skip), wait_limit_ns))
