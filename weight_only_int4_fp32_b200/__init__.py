@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 __all__ = [
     "LING_MOE_OK", "LING_MOE_ERR_INVALID_ARG", "LING_MOE_ERR_CUDA", "LING_MOE_ERR_OOM",
@@ -158,8 +159,8 @@ def _load():
         "ling_moe_beam_launch_count": (i64, [vp]),
         "ling_moe_beam_destroy": (None, [vp]),
         "ling_moe_delta_create": (ci, [ctypes.POINTER(ling_moe_delta_config_t), ctypes.POINTER(vp)]),
-        "ling_moe_delta_step": (ci, [vp, ctypes.POINTER(ling_moe_delta_io_t), ci, ci, vp, vp]),
-        "ling_moe_delta_prefill": (ci, [vp, ctypes.POINTER(ling_moe_delta_io_t), ci, vp, ci, vp, vp]),
+        "ling_moe_delta_step": (ci, [vp, vp, ci, ci, vp, vp]),
+        "ling_moe_delta_prefill": (ci, [vp, vp, ci, vp, ci, vp, vp]),
         "ling_moe_delta_status": (ci, [vp, vp]),
         "ling_moe_delta_launch_count": (i64, [vp]),
         "ling_moe_delta_destroy": (None, [vp]),
@@ -184,7 +185,9 @@ def _load():
 
 class _LazyLib:
     def __getattr__(self, name):
-        return getattr(load_library(), name)
+        f = getattr(load_library(), name)
+        setattr(self, name, f)  # found without this call from now on
+        return f
 
 
 lib = _LazyLib()
@@ -296,7 +299,7 @@ def ling_moe_route_noalloc_test_set_wait(skip_cta: int, wait_limit_ns: int) -> i
 def _require(t, shape, dtype, cuda: bool, name: str):
     """Raise ValueError unless t is a contiguous tensor of this shape and dtype
     on the GPU (cuda) or the host; the C calls trust the sizes they are given."""
-    if (tuple(t.shape) != tuple(shape) or t.dtype != dtype or bool(t.is_cuda) != cuda
+    if (t.shape != tuple(shape) or t.dtype != dtype or t.is_cuda != cuda
             or not t.is_contiguous()):
         where = "CUDA" if cuda else "host"
         raise ValueError(f"{name} must be a contiguous {where} {dtype} tensor of shape {tuple(shape)}, "
@@ -531,7 +534,7 @@ class LMHeadFP8:
 
 def _raw_stream(torch, stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return getattr(stream, "cuda_stream", stream)
 
 
@@ -541,6 +544,18 @@ def _on_current_device(torch, name, *tensors):
     for t in tensors:
         if t is not None and t.get_device() != cur:
             raise ValueError(f"{name}: a tensor on {t.device}, the current device is cuda:{cur}")
+
+
+def _new(torch, like, shape, dtype, stream):
+    """An output tensor on `like`'s device (shape None: like's own), whose memory belongs to the stream that
+    writes it: on another one, memory that the current stream has just given back could still be in use."""
+    if stream is not None:
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream)
+        with torch.cuda.stream(s):
+            return _new(torch, like, shape, dtype, None)
+    if shape is None:  # the quickest call
+        return torch.empty_like(like, dtype=dtype)
+    return like.new_empty(shape, dtype=dtype)
 
 
 class _Handle:
@@ -589,8 +604,9 @@ class BeamSearch(_Handle):
         W, V = self.beams, self.vocab
         if logits.dim() == 2 and logits.shape[0] % W == 0:
             logits = logits.unflatten(0, (logits.shape[0] // W, W))
-        if (logits.dim() != 3 or tuple(logits.shape[1:]) != (W, V) or not logits.is_cuda
-                or logits.dtype not in (torch.float32, torch.bfloat16) or (V > 1 and logits.stride(2) != 1)):
+        dt = logits.dtype
+        if (logits.dim() != 3 or logits.shape != (logits.shape[0], W, V) or not logits.is_cuda
+                or (dt != torch.float32 and dt != torch.bfloat16) or (V > 1 and logits.stride(2) != 1)):
             raise ValueError(f"logits must be a CUDA fp32 or bf16 tensor [groups, {W}, {V}] or [groups * {W}, {V}], "
                              f"contiguous along the vocabulary, got {logits.dtype} {tuple(logits.shape)}")
         G = logits.shape[0]
@@ -600,12 +616,11 @@ class BeamSearch(_Handle):
                 raise ValueError("finished must be bool or uint8")
             _require(finished, (G, W), finished.dtype, True, "finished")
         _on_current_device(torch, "select", logits, scores, finished)
-        new = lambda dt: torch.empty((G, W), dtype=dt, device=logits.device)  # noqa: E731
-        tokens, parents, out, done = new(torch.int32), new(torch.int32), new(torch.float32), new(torch.bool)
+        tokens, parents, out, done = (_new(torch, scores, None, t, stream)
+                                      for t in (torch.int32, torch.int32, torch.float32, torch.bool))
         _check(lib.ling_moe_beam_select(
             self.handle, logits.data_ptr(),
-            LING_MOE_TYPE_F32 if logits.dtype == torch.float32 else LING_MOE_TYPE_BF16, logits.stride(0),
-            logits.stride(1), G, scores.data_ptr(), finished.data_ptr() if finished is not None else None, int(eos),
+            LING_MOE_TYPE_F32 if dt == torch.float32 else LING_MOE_TYPE_BF16, logits.stride(0), logits.stride(1), G, scores.data_ptr(), finished.data_ptr() if finished is not None else None, int(eos),
             tokens.data_ptr(), parents.data_ptr(), out.data_ptr(), done.data_ptr(), _raw_stream(torch, stream)))
         return tokens, parents, out, done
 
@@ -671,22 +686,21 @@ class BlockFP8Linear(_Handle):
         (default) or fp32; out: a tensor to write, rows may be strided."""
         torch = self._torch
         N, K = self.out_features, self.in_features
-        if (x.dim() != 2 or x.shape[1] != K or x.dtype != torch.bfloat16 or not x.is_cuda
-                or (K > 1 and x.stride(1) != 1)):
+        T = x.shape[0] if x.dim() == 2 else -1
+        if x.shape != (T, K) or x.dtype != torch.bfloat16 or not x.is_cuda or (K > 1 and x.stride(1) != 1):
             raise ValueError(f"x must be a CUDA bf16 tensor [T, {K}] with contiguous rows, got {x.dtype} "
                              f"{tuple(x.shape)} on {x.device}")
-        T = x.shape[0]
-        if out is None:
-            out = torch.empty((T, N), dtype=out_dtype or torch.bfloat16, device=x.device)
-        if (tuple(out.shape) != (T, N) or out.dtype not in (torch.bfloat16, torch.float32)
-                or out.dtype != (out_dtype or out.dtype) or not out.is_cuda or (N > 1 and out.stride(1) != 1)):
-            raise ValueError(f"out must be a CUDA bf16 or fp32 tensor [{T}, {N}] with contiguous rows, got {out.dtype} "
-                             f"{tuple(out.shape)} on {out.device}")
+        bf16 = (out_dtype if out is None else out.dtype) in (None, torch.bfloat16)
+        if out is None and out_dtype in (None, torch.bfloat16, torch.float32):
+            out = _new(torch, x, (T, N), torch.bfloat16 if bf16 else torch.float32, stream)
+        elif (out is None or out.shape != (T, N) or out.dtype not in (torch.bfloat16, torch.float32)
+              or out.dtype != (out_dtype or out.dtype) or not out.is_cuda or (N > 1 and out.stride(1) != 1)):
+            raise ValueError(f"out must be a CUDA bf16 or fp32 tensor [{T}, {N}] with contiguous rows, got "
+                             + (f"{out.dtype} {tuple(out.shape)} on {out.device}" if out is not None else f"{out_dtype}"))
         _on_current_device(torch, "forward", x, out)
         _check(lib.ling_moe_fp8_linear_forward(
-            self.handle, x.data_ptr(), x.stride(0), T, out.data_ptr(),
-            LING_MOE_TYPE_BF16 if out.dtype == torch.bfloat16 else LING_MOE_TYPE_F32, out.stride(0),
-            _raw_stream(torch, stream)))
+            self.handle, x.data_ptr(), x.stride(0), T, out.data_ptr(), LING_MOE_TYPE_BF16 if bf16 else LING_MOE_TYPE_F32,
+            out.stride(0), _raw_stream(torch, stream)))
         return out
 
     __call__ = forward
@@ -729,38 +743,46 @@ class GatedDeltaRule(_Handle):
         self.handle = h.value
         self._torch = torch
 
-    def _io(self, lead, q, k, v, g, beta, state, slots, seqs, out):
-        """Check the tensors of a call with leading dimensions `lead` and fill its ling_moe_delta_io_t."""
+    # ling_moe_delta_io_t: pointers of q, k, v, g, beta; their strides; g's channel stride; out, state; slots
+    _pack = struct.Struct("@5P15qqPPiP").pack
+
+    def _io(self, lead, q, k, v, g, beta, state, slots, seqs, out, stream):
+        """Check the tensors of a call with leading dimensions `lead` (a tuple); its ling_moe_delta_io_t as bytes, and out."""
         torch = self._torch
         Hk, Hv, dk, dv = self.k_heads, self.v_heads, self.head_k, self.head_v
         nl = len(lead)
-        gc = 1 if g.dim() == nl + 2 else 0
-        for name, t, tail, dt in (("q", q, (Hk, dk), torch.bfloat16), ("k", k, (Hk, dk), torch.bfloat16),
-                                  ("v", v, (Hv, dv), torch.bfloat16), ("g", g, (Hv, dk) if gc else (Hv,), torch.float32),
-                                  ("beta", beta, (Hv,), torch.float32)):
-            if t.shape != lead + tail or t.dtype != dt or not t.is_cuda:
-                raise ValueError(f"{name} must be a CUDA {dt} tensor of shape {tuple(lead + tail)}, got {t.dtype} "
+        gc = g.dim() == nl + 2
+        dev = torch.cuda.current_device() if q.is_cuda else -2
+        bf16, f32 = torch.bfloat16, torch.float32
+        qk = (*lead, Hk, dk)
+        vh, bh = (*lead, Hv, dv), (*lead, Hv)
+        for name, t, shape, dt in (("q", q, qk, bf16), ("k", k, qk, bf16), ("v", v, vh, bf16),
+                                   ("g", g, (*lead, Hv, dk) if gc else bh, f32), ("beta", beta, bh, f32)):
+            if t.shape != shape or t.dtype != dt or t.get_device() != dev:
+                raise ValueError(f"{name} must be a CUDA {dt} tensor of shape {shape} on the current device, got {t.dtype} "
                                  f"{tuple(t.shape)} on {t.device}")
-        for name, t in (("q", q), ("k", k), ("v", v)):
-            if t.stride(-1) != 1:
-                raise ValueError(f"{name} must be contiguous along its last dimension")
-        if gc and g.stride(-1) not in (0, 1):
+        sq, sk, sv, sg, sb = q.stride(), k.stride(), v.stride(), g.stride(), beta.stride()
+        if sq[-1] != 1 or sk[-1] != 1 or sv[-1] != 1:
+            raise ValueError("q, k and v must be contiguous along their last dimension")
+        if gc and sg[-1] not in (0, 1):
             raise ValueError("g must be contiguous (or expanded) along its last dimension")
-        if (state.dim() != 4 or state.shape[1:] != (Hv, dk, dv) or state.dtype != torch.float32 or not state.is_cuda
-                or not state.is_contiguous()):
-            raise ValueError(f"state must be a contiguous CUDA float32 tensor [slots, {Hv}, {dk}, {dv}], got {state.dtype} "
-                             f"{tuple(state.shape)} on {state.device}")
+        if (state.shape != (state.shape[0] if state.dim() else 0, Hv, dk, dv) or state.dtype != f32
+                or state.get_device() != dev or not state.is_contiguous()):
+            raise ValueError(f"state must be a contiguous CUDA float32 tensor [slots, {Hv}, {dk}, {dv}] on the current "
+                             f"device, got {state.dtype} {tuple(state.shape)} on {state.device}")
         if slots is not None:
             _require(slots, (seqs,), torch.int32, True, "slots")
         if out is None:
-            out = torch.empty(lead + (Hv, dv), dtype=torch.bfloat16, device=q.device)
+            out = _new(torch, q, vh, bf16, stream)
         else:
-            _require(out, lead + (Hv, dv), torch.bfloat16, True, "out")
-        _on_current_device(torch, "delta rule", q, k, v, g, beta, state, slots, out)
-        st = lambda t: tuple(t.stride()[:3]) if nl == 2 else (0, t.stride(0), t.stride(1))  # noqa: E731
-        io = ling_moe_delta_io_t(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), st(q), st(k),
-                                 st(v), st(g), st(beta), g.stride(-1) if gc else 0, out.data_ptr(), state.data_ptr(),
-                                 state.shape[0], slots.data_ptr() if slots is not None else None)
+            _require(out, vh, bf16, True, "out")
+        if slots is not None or out.get_device() != dev:
+            _on_current_device(torch, "delta rule", slots, out)
+        if nl == 1:  # no dimension of sequences
+            sq, sk, sv, sg, sb = (0, *sq), (0, *sk), (0, *sv), (0, *sg), (0, *sb)
+        io = self._pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), *sq[:3], *sk[:3], *sv[:3],
+                        *sg[:3], *sb, sg[3] if gc else 0, out.data_ptr(), state.data_ptr(), state.shape[0],
+                        slots.data_ptr() if slots is not None else 0)
         return io, out
 
     def step(self, q, k, v, g, beta, state, slots=None, accepted=None, out=None, stream=None):
@@ -771,12 +793,12 @@ class GatedDeltaRule(_Handle):
         torch = self._torch
         if q.dim() != 4:
             raise ValueError("q must be 4-D [sequences, tokens, heads, head_k]")
-        B, n = q.shape[:2]
-        io, out = self._io(q.shape[:2], q, k, v, g, beta, state, slots, B, out)
+        B, n = q.shape[0], q.shape[1]
+        io, out = self._io((B, n), q, k, v, g, beta, state, slots, B, out, stream)
         if accepted is not None:
             _require(accepted, (B,), torch.int32, True, "accepted")
             _on_current_device(torch, "step", accepted)
-        _check(lib.ling_moe_delta_step(self.handle, ctypes.byref(io), B, n,
+        _check(lib.ling_moe_delta_step(self.handle, io, B, n,
                                        accepted.data_ptr() if accepted is not None else None,
                                        _raw_stream(torch, stream)))
         return out
@@ -796,9 +818,9 @@ class GatedDeltaRule(_Handle):
             if fresh.dtype not in (torch.bool, torch.uint8):
                 raise ValueError("fresh must be bool or uint8")
             _require(fresh, (S,), fresh.dtype, True, "fresh")
-        io, out = self._io(q.shape[:1], q, k, v, g, beta, state, slots, S, out)
+        io, out = self._io((q.shape[0],), q, k, v, g, beta, state, slots, S, out, stream)
         _on_current_device(torch, "prefill", cu_seqlens, fresh)
-        _check(lib.ling_moe_delta_prefill(self.handle, ctypes.byref(io), q.shape[0], cu_seqlens.data_ptr(), S,
+        _check(lib.ling_moe_delta_prefill(self.handle, io, q.shape[0], cu_seqlens.data_ptr(), S,
                                           fresh.data_ptr() if fresh is not None else None,
                                           _raw_stream(torch, stream)))
         return out
