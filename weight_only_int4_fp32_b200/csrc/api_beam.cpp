@@ -90,9 +90,11 @@ int ling_moe_beam_select(ling_moe_beam_t* h, const void* logits, int logits_type
   }
   if (int rc = check_same_device(h->device)) return rc;
 
-  // Segments: about 8 CTAs per SM over the whole call, each at least one tile.
-  const int tiles = (h->vocab + kBeamTile - 1) / kBeamTile;
-  int segs = (int)((8ll * h->sms + (long long)rows - 1) / (long long)rows);
+  // Segments: as many as keep the whole call within one wave of CTAs (kBeamCtas
+  // per SM), each at least one tile.
+  const int tile = beam_tile(logits_type == LING_MOE_TYPE_BF16), tiles = (h->vocab + tile - 1) / tile;
+  int segs = (int)((long long)kBeamCtas * h->sms / (long long)rows);
+  if (segs < 1) segs = 1;
   if (segs > kBeamMaxSegs) segs = kBeamMaxSegs;
   if (segs > tiles) segs = tiles;
   const int per = (tiles + segs - 1) / segs;
@@ -108,7 +110,7 @@ int ling_moe_beam_select(ling_moe_beam_t* h, const void* logits, int logits_type
   p.vocab = h->vocab;
   p.eos = eos;
   p.segs = segs;
-  p.seg_len = per * kBeamTile;
+  p.seg_len = per * tile;
   p.parts = h->parts;
   p.arrived = h->arrived;
   p.tokens = tokens;

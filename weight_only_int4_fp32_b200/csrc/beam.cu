@@ -11,15 +11,19 @@
 // logits themselves, ties to the lower token, whatever the scores round to.
 //
 // One pass over the logits, one launch.  A row is cut into segments of whole
-// tiles of 4096 logits; a CTA walks one segment with the tile in registers,
-// keeping per thread the running (max, sum) and per CTA the best W keys.  A
+// tiles of 4096 (bf16: 8192) logits; a CTA walks one segment, each thread
+// keeping the (max, sum) of its own logits, with nothing shared on the way.
+// The W-th largest of the 256 threads' maxima is a bound that W candidates
+// reach, and only the few threads whose maximum reaches it own such candidates:
+// their logits are read once more (from L2; 8 of 256) and the best W kept.  A
 // key is (order key of the logit, ~token): all distinct, larger is better.
-// Only keys above the W-th best so far (tau) are looked at: from the second
-// tile on that is a handful per tile.  Where many threads exceed tau (the
-// first tile, ascending rows) it is raised first to the W-th largest of 32
-// group maxima, which bounds what can pass to W groups x 128 keys.  The last
-// CTA of a group to finish merges: a warp per row joins the segments' sums
-// and merges their sorted lists (a lane per segment), then one warp merges
+// Where equal logits let too many through, the segment is walked a second time
+// with a bound on whole keys, tau, that rises as keys are found: where many
+// threads exceed it, it becomes the W-th largest of 32 group maxima first,
+// which bounds what can pass to W groups x 8 threads' keys; the buffer is cut to
+// its best W, and tau raised to the W-th, when the next tile might not fit.
+// The last CTA of a group to finish merges: a warp per row joins the segments'
+// sums and merges their sorted lists (a lane per segment), then one warp merges
 // the rows (a lane per row).
 //
 // Bound: HBM for large batches, latency (one tile, two merges) for one
@@ -33,17 +37,22 @@ namespace lingmoe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPerThread = kBeamTile / kThreads;             // 16
-constexpr int kBufKeys = kBeamMax + kBeamMax * 8 * kPerThread;  // kept + W groups of 8 threads
-constexpr int kManyHits = 64;                                // threads that may push without raising tau
-static_assert(kManyHits * kPerThread <= kBeamMax * 8 * kPerThread, "push bound");
+constexpr int kManyHits = 64;                          // threads that may push without raising tau
+constexpr int kBufKeys = kBeamMax + kBeamMax * 8 * 32;  // what is kept, and what a tile may push: W groups of 8 threads
+constexpr int kChosen = 32;                            // threads whose logits are read once more
 constexpr unsigned long long kNoKey = 0x007FFFFFFFFFFFFFull;  // every key of a logit above -inf is larger
 constexpr float kLowest = -3.402823466e38f;
 
-// 16 logits per thread, NV vectors of 16 bytes
+// a thread's logits of a tile: 4 vectors of 16 bytes
 template <bool BF16> struct Tile;
 template <> struct Tile<false> {
-  static constexpr int kVecs = 4, kVec = 4;
+  static constexpr int kVecs = 4, kVec = 4, kPer = 16, kLogits = beam_tile(false);
+  __device__ static float max(const uint4* r) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) m = fmaxf(m, get(r, e));
+    return m;
+  }
   __device__ static float get(const uint4* r, int e) {
     const uint4& v = r[e >> 2];
     const uint32_t b = (e & 3) == 0 ? v.x : (e & 3) == 1 ? v.y : (e & 3) == 2 ? v.z : v.w;
@@ -51,7 +60,20 @@ template <> struct Tile<false> {
   }
 };
 template <> struct Tile<true> {
-  static constexpr int kVecs = 2, kVec = 8;
+  static constexpr int kVecs = 4, kVec = 8, kPer = 32, kLogits = beam_tile(true);
+  // the largest of a tile (NaN aside), two at a time
+  __device__ static float max(const uint4* r) {
+    __nv_bfloat162 m[2];
+    m[0] = m[1] = __halves2bfloat162(__ushort_as_bfloat16(0xFF80u), __ushort_as_bfloat16(0xFF80u));
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+      const uint32_t w[4] = {r[v].x, r[v].y, r[v].z, r[v].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m[i & 1] = __hmax2(m[i & 1], *reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+    }
+    m[0] = __hmax2(m[0], m[1]);
+    return fmaxf(__low2float(m[0]), __high2float(m[0]));
+  }
   __device__ static float get(const uint4* r, int e) {
     const uint4& v = r[e >> 3];
     const int k = (e & 7) >> 1;
@@ -65,34 +87,67 @@ template <bool BF16> __device__ __forceinline__ int tile_at(int tid, int e) {
   return (e / VE) * (kThreads * VE) + tid * VE + e % VE;
 }
 
-// The tile that starts at `base`, logits at and past `end` as -inf.  The
-// element a thread gets does not depend on the row's alignment.
+// the vector of logits i .. of a row, those at and past `end` as -inf
 template <bool BF16>
-__device__ __forceinline__ void load_tile(uint4* r, const unsigned char* row, int base, int end, int tid, bool al) {
+__device__ __forceinline__ void load_vec(uint4& r, const unsigned char* row, int i, int end, bool al) {
   constexpr int VE = Tile<BF16>::kVec, ES = BF16 ? 2 : 4;
+  if (al && i + VE <= end) {
+    r = ldg_stream(row + (size_t)i * ES);
+  } else {
+    uint32_t w[4];
 #pragma unroll
-  for (int v = 0; v < Tile<BF16>::kVecs; ++v) {
-    const int i = base + v * (kThreads * VE) + tid * VE;
-    if (al && i + VE <= end) {
-      r[v] = ldg_stream(row + (size_t)i * ES);
-    } else {
-      uint32_t w[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if constexpr (BF16) {
-          const unsigned short* p = reinterpret_cast<const unsigned short*>(row);
-          const uint32_t lo = i + 2 * k < end ? p[i + 2 * k] : 0xFF80u;
-          const uint32_t hi = i + 2 * k + 1 < end ? p[i + 2 * k + 1] : 0xFF80u;
-          w[k] = lo | (hi << 16);
-        } else {
-          w[k] = i + k < end ? reinterpret_cast<const uint32_t*>(row)[i + k] : 0xFF800000u;
-        }
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (BF16) {
+        const unsigned short* p = reinterpret_cast<const unsigned short*>(row);
+        const uint32_t lo = i + 2 * k < end ? p[i + 2 * k] : 0xFF80u;
+        const uint32_t hi = i + 2 * k + 1 < end ? p[i + 2 * k + 1] : 0xFF80u;
+        w[k] = lo | (hi << 16);
+      } else {
+        w[k] = i + k < end ? reinterpret_cast<const uint32_t*>(row)[i + k] : 0xFF800000u;
       }
-      r[v] = make_uint4(w[0], w[1], w[2], w[3]);
     }
+    r = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
+// The tile that starts at `base`.  The element a thread gets does not depend on
+// the row's alignment.
+template <bool BF16>
+__device__ __forceinline__ void load_tile(uint4* r, const unsigned char* row, int base, int end, int tid, bool al) {
+  constexpr int VE = Tile<BF16>::kVec;
+#pragma unroll
+  for (int v = 0; v < Tile<BF16>::kVecs; ++v) load_vec<BF16>(r[v], row, base + v * (kThreads * VE) + tid * VE, end, al);
+}
 
+// two floats in one register pair, and the same operation on both
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pack2(float x, float y) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+// exp(x), x <= 0, to 2 ulp of the result (and 2^-24 |x| for the product); arguments below 2^-126 count as 0
+__device__ __forceinline__ float exp_neg(float x) { return ex2(x * kLog2e); }
 // NaN counts as -inf; -0 as +0 (equal logits tie)
 __device__ __forceinline__ float clean(float z) { return fmaxf(z, -INFINITY) + 0.0f; }
 __device__ __forceinline__ unsigned long long make_key(float z, int token) {
@@ -116,6 +171,10 @@ struct SelectSmem {
   };
   unsigned long long best[kBeamMax];
   unsigned long long grp[32];
+  __align__(16) uint32_t tops[kThreads];
+  int who[kChosen];
+  int chosen;
+  uint32_t bound;
   unsigned long long tau;
   unsigned long long row_key[kBeamMax][kBeamMax];
   double row_score[kBeamMax][kBeamMax];
@@ -141,7 +200,7 @@ __device__ __forceinline__ void keep_best(SelectSmem& sm, int K, int tid) {
   if (tid < K) sm.buf[tid] = sm.best[tid];
   if (tid == 0) {
     sm.count = n < K ? n : K;
-    if (n >= K) sm.tau = sm.best[K - 1];
+    if (n >= K && sm.best[K - 1] > sm.tau) sm.tau = sm.best[K - 1];
   }
   __syncthreads();
 }
@@ -149,7 +208,7 @@ __device__ __forceinline__ void keep_best(SelectSmem& sm, int K, int tid) {
 }  // namespace
 
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) beam_select_kernel(const BeamSelectParams p) {
+__global__ void __launch_bounds__(kThreads, kBeamCtas) beam_select_kernel(const BeamSelectParams p) {
   __shared__ SelectSmem sm;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row = blockIdx.x / p.segs, seg = blockIdx.x % p.segs;
@@ -157,6 +216,10 @@ __global__ void __launch_bounds__(kThreads) beam_select_kernel(const BeamSelectP
   const int K = p.beams;
   const float score = p.scores[row];
   const bool live = score > -INFINITY && !(p.finished && p.finished[row]);  // false for NaN
+  constexpr int NV = Tile<BF16>::kVecs, VE = Tile<BF16>::kVec;
+  constexpr int kPerThread = Tile<BF16>::kPer, kBeamTile = Tile<BF16>::kLogits;
+  constexpr int kTilePush = kBeamMax * 8 * kPerThread;
+  static_assert(kManyHits * kPerThread <= kTilePush && kBeamMax + kTilePush <= kBufKeys, "push bound");
   BeamPart* part = p.parts + (size_t)row * p.segs + seg;
 
   if (live) {
@@ -167,35 +230,116 @@ __global__ void __launch_bounds__(kThreads) beam_select_kernel(const BeamSelectP
     const int end = min(p.vocab, begin + p.seg_len);
     if (tid == 0) {
       sm.count = 0;
+      sm.chosen = 0;
       sm.tau = kNoKey;
     }
-    float m = kLowest, s = 0.f;
-    uint4 cur[Tile<BF16>::kVecs], nxt[Tile<BF16>::kVecs];
-    load_tile<BF16>(cur, z, begin, end, tid, al);
+    // ---- one pass: the thread's largest logit and its sum of exp
+    float m = kLowest, s = 0.f, top = -INFINITY;
+    {
+      uint4 cur[NV], nxt[NV];
+      load_tile<BF16>(cur, z, begin, end, tid, al);
+      for (int base = begin; base < end; base += kBeamTile) {
+        if (base + kBeamTile < end) load_tile<BF16>(nxt, z, base + kBeamTile, end, tid, al);
+        const float mx = Tile<BF16>::max(cur);
+        top = fmaxf(top, mx);
+        const float mn = fmaxf(m, mx);
+        s *= exp_neg(m - mn);
+        m = mn;
+        f2 t[2] = {0ull, 0ull};
+        const f2 off = pack2(-m, -m), scale = pack2(kLog2e, kLog2e);
+#pragma unroll
+        for (int e = 0; e < kPerThread; e += 2) {
+          const float2 x = unpack2(mul2(add2(pack2(Tile<BF16>::get(cur, e), Tile<BF16>::get(cur, e + 1)), off), scale));
+          t[(e >> 1) & 1] = add2(t[(e >> 1) & 1], pack2(ex2(x.x), ex2(x.y)));
+        }
+        const float2 ts = unpack2(add2(t[0], t[1]));
+        float sum = ts.x + ts.y;
+        if (!(sum == sum)) {  // a NaN among them: it counts as -inf
+          sum = 0.f;
+#pragma unroll 1
+          for (int v = 0; v < NV; ++v) {
+            const uint4 one[1] = {v == 0 ? cur[0] : v == 1 ? cur[1] : v == 2 ? cur[2] : cur[3]};
+#pragma unroll
+            for (int e = 0; e < VE; ++e) sum += exp_neg(fmaxf(Tile<BF16>::get(one, e), -INFINITY) - m);
+          }
+        }
+        s += sum;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) cur[v] = nxt[v];
+      }
+    }
+    // ---- the K-th largest of the threads' maxima: K candidates reach it, and
+    // whatever does belongs to a thread that does
+    // (the order keys' low 8 bits give way to the thread, so that all differ; the
+    // bound is that much lower at most)
+    const uint32_t mine = (f32_order_key(clean(top)) & ~255u) | (uint32_t)tid;
+    sm.tops[tid] = mine;
     __syncthreads();
-    unsigned long long tau = sm.tau;
-    for (int base = begin; base < end; base += kBeamTile) {
-      if (base + kBeamTile < end) load_tile<BF16>(nxt, z, base + kBeamTile, end, tid, al);
-      float mx = -INFINITY;
+    if (warp == 0) {
+      uint32_t k[kThreads / 32], best = 0u;
 #pragma unroll
-      for (int e = 0; e < kPerThread; ++e) mx = fmaxf(mx, Tile<BF16>::get(cur, e));
-      const float mn = fmaxf(m, mx);
-      s *= __expf(m - mn);
-      m = mn;
+      for (int i = 0; i < kThreads / 32; ++i) k[i] = sm.tops[32 * i + lane];
+      for (int i = 0; i < K; ++i) {
+        uint32_t own = 0u;
 #pragma unroll
-      for (int e = 0; e < kPerThread; ++e) s += __expf(clean(Tile<BF16>::get(cur, e)) - m);
-      bool hit = f32_order_key(clean(mx)) >= (uint32_t)(tau >> 32) && mx > -INFINITY;
-      const int hits = __syncthreads_count(hit);
-      if (hits) {
+        for (int j = 0; j < kThreads / 32; ++j) own = k[j] > own ? k[j] : own;
+        best = __reduce_max_sync(0xffffffffu, own);
+#pragma unroll
+        for (int j = 0; j < kThreads / 32; ++j) k[j] = k[j] == best ? 0u : k[j];
+      }
+      if (lane == 0) sm.bound = best & ~255u;
+    }
+    __syncthreads();
+    const uint32_t bound = sm.bound;
+    if (mine >= bound && top > -INFINITY) {
+      const int at = atomicAdd(&sm.chosen, 1);
+      if (at < kChosen) sm.who[at] = tid;
+    }
+    __syncthreads();
+    const int chosen = sm.chosen;
+    // ---- those threads' logits once more, a vector at a time
+    if (chosen <= kChosen) {
+      const int tiles = (end - begin + kBeamTile - 1) / kBeamTile;
+      const float boundf = bound > f32_order_key(-INFINITY) ? f32_from_order_key(bound) : -INFINITY;
+      for (int i = tid; i < chosen * tiles * NV; i += kThreads) {
+        const int v = i % NV, t = i / NV % tiles, owner = sm.who[i / NV / tiles];
+        const int at = begin + t * kBeamTile + v * (kThreads * VE) + owner * VE;
+        uint4 one[1];
+        load_vec<BF16>(one[0], z, at, end, al);
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          const float x = clean(Tile<BF16>::get(one, e));
+          if (x >= boundf && x > -INFINITY) {
+            const int slot = atomicAdd(&sm.count, 1);
+            if (slot < kBufKeys) sm.buf[slot] = make_key(x, at + e);
+          }
+        }
+      }
+      __syncthreads();
+    }
+    // ---- many equal logits: too many threads or candidates reach the bound; tile by tile with a rising tau
+    if (chosen > kChosen || sm.count > kBufKeys) {
+      __syncthreads();
+      if (tid == 0) sm.count = 0;
+      __syncthreads();
+      unsigned long long tau = kNoKey;
+      int held = 0;  // the buffer has at most this many keys (the same in every thread)
+#pragma unroll 1
+      for (int base = begin; base < end; base += kBeamTile) {
+        uint4 cur[NV];
+        load_tile<BF16>(cur, z, base, end, tid, al);
+        // the thread's best key of the tile
+        unsigned long long best = 0ull;
+#pragma unroll
+        for (int e = 0; e < kPerThread; ++e) {
+          const unsigned long long k = make_key(clean(Tile<BF16>::get(cur, e)), base + tile_at<BF16>(tid, e));
+          if (k > best) best = k;
+        }
+        const bool hit = best > tau;
+        const int hits = __syncthreads_count(hit);
+        if (!hits) continue;
         if (hits > kManyHits) {
           // raise tau to just below the K-th largest of 32 group maxima
-          unsigned long long best = 0ull;
-#pragma unroll
-          for (int e = 0; e < kPerThread; ++e) {
-            const float v = clean(Tile<BF16>::get(cur, e));
-            const unsigned long long k = make_key(v, base + tile_at<BF16>(tid, e));
-            if (k > best) best = k;
-          }
 #pragma unroll
           for (int o = 1; o < 8; o <<= 1) {
             const unsigned long long x = __shfl_xor_sync(0xffffffffu, best, o);
@@ -206,32 +350,34 @@ __global__ void __launch_bounds__(kThreads) beam_select_kernel(const BeamSelectP
           if (warp == 0) {
             const unsigned long long k = sm.grp[lane];
             int r = 0;
-#pragma unroll 8
-            for (int j = 0; j < 32; ++j) r += __shfl_sync(0xffffffffu, k, j) > k;
-            if (r == K - 1 && k - 1 > sm.tau) sm.tau = k - 1;  // keys are distinct: one lane
+            for (int j = 0; j < 32; ++j) r += sm.grp[j] > k;
+            if (r == K - 1 && k - 1 > sm.tau) sm.tau = k - 1;  // keys of logits above -inf are distinct: one lane
           }
           __syncthreads();
           tau = sm.tau;
         }
+        const int push = hits > kManyHits ? kTilePush : hits * kPerThread;
+        if (held + push > kBufKeys) {  // what earlier tiles pushed stands: a barrier since
+          keep_best(sm, K, tid);
+          tau = sm.tau;
+          held = K;
+        }
+        held += push;
         if (hit) {
 #pragma unroll
           for (int e = 0; e < kPerThread; ++e) {
-            const float v = clean(Tile<BF16>::get(cur, e));
-            const unsigned long long k = make_key(v, base + tile_at<BF16>(tid, e));
-            if (k > tau && v > -INFINITY) {
+            const float x = clean(Tile<BF16>::get(cur, e));
+            const unsigned long long k = make_key(x, base + tile_at<BF16>(tid, e));
+            if (k > tau && x > -INFINITY) {
               const int at = atomicAdd(&sm.count, 1);
               if (at < kBufKeys) sm.buf[at] = k;
             }
           }
         }
-        __syncthreads();
-        if (sm.count > K) keep_best(sm, K, tid);
-        tau = sm.tau;
       }
-#pragma unroll
-      for (int v = 0; v < Tile<BF16>::kVecs; ++v) cur[v] = nxt[v];
+      __syncthreads();
     }
-    keep_best(sm, K, tid);  // at most K keys: sorts them
+    keep_best(sm, K, tid);
     // the segment's max and sum, joined in 64 bits
     float bm = m;
 #pragma unroll

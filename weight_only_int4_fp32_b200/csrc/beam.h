@@ -11,7 +11,8 @@ namespace lingmoe {
 
 constexpr int kBeamMax = 16;        // beams per group
 constexpr int kBeamMaxSegs = 32;    // pieces of a row, one lane each in the merge
-constexpr int kBeamTile = 4096;     // logits a CTA takes at a time: 256 threads x 16
+constexpr int beam_tile(bool bf16) { return bf16 ? 8192 : 4096; }  // logits a CTA takes at a time: 256 threads x 64 bytes
+constexpr int kBeamCtas = 4;        // CTAs of the selection that an SM holds at once
 constexpr int kReorderTensors = 32; // tensors per reorder launch
 
 // One piece of a row: its largest logit, sum of exp(logit - max), and its best
