@@ -53,10 +53,10 @@ def step_bound(q, k, v, g, beta, state, scale):
 
     exp is off by 2 ulp (4 u) and its product by 1 u; a unit key by 9 u (a sum of
     squares in 9 additions, halved by the root; root, sum with the 1e-6, quotient,
-    product); S^T k adds 13 u in its chain of 8 products and 5 joins, so it is
-    off by 27 u |S|; v - x and beta by 2 u (|v| + |S|); k u^T by the key's 9 u,
-    and its sum by 1 u more.  The output takes a query (9 u) and k.q (9 + 18 u)
-    with two more roundings."""
+    product); S^T k adds 19 u in its chain of 16 products and 3 joins, so it is
+    off by 33 u |S|; v - x and beta by 2 u (|v| + |S|); k u^T by the key's 9 u,
+    and its sum by 1 u more.  The output takes S^T q (33 u) and k.q (9 + 18 u)
+    with three more roundings."""
     q, k, v, a, b = heads(q, k, v, g, beta)
     S = np.asarray(state, np.float64).copy()
     e = np.zeros((S.shape[0], S.shape[2]))
@@ -68,9 +68,9 @@ def step_bound(q, k, v, g, beta, state, scale):
         u = b[t][:, None] * (v[t] - np.einsum("hkv,hk->hv", S, k[t]))
         S = S + k[t][:, :, None] * u[:, None, :]
         size = S0 + np.abs(v[t])
-        du = 29 * U * bt * size
+        du = 35 * U * bt * size
         e = a[t].max(-1)[:, None] * e + 6 * U * S0 + du + 11 * U * np.abs(u) + 1e-37
-        out[t] = abs(scale) * (e + 30 * U * S0 + du + 32 * U * np.abs(u)) * (1 + 4 * U)
+        out[t] = abs(scale) * (e + 36 * U * S0 + du + 32 * U * np.abs(u)) * (1 + 4 * U)
         es[t] = e
     return out, es
 

@@ -407,3 +407,39 @@ def test_refusals_and_wait_timeout():
     f.test_set_wait(False)
     assert torch.equal(f.prefill(*a, s2, cu), y) and torch.equal(s1, s2) and f.status() == lm.LING_MOE_OK
     f.close()
+
+
+@pytest.mark.parametrize("dk,dv,n", [(64, 64, 1), (128, 128, 4), (128, 64, 8), (64, 128, 5)])
+def test_step_of_many_heads(dk, dv, n):
+    """More heads than fit the GPU at once: the same bits as a few sequences at a time, padding and all."""
+    Hk, Hv, B = 2, 8, 130
+    f = lm.GatedDeltaRule(Hk, Hv, dk, dv, 8, B)
+    a = [t.view(B, n, *t.shape[1:]) for t in make(B * n, Hk, Hv, dk, dv, True, 20)]
+    st = pool(B, Hv, dk, dv, 20)
+    slots = torch.randperm(B, generator=torch.Generator().manual_seed(1)).int()
+    slots[[0, 5, 37, 38, 39, 40, 129]] = torch.tensor([-1, B, -7, -7, 2**31 - 1, -(2**31), -1], dtype=torch.int32)
+    slots = slots.to(DEV)
+    acc = (torch.arange(B, device=DEV) % (n + 1)).int()
+    big, small = st.clone(), st.clone()
+    o1 = torch.full((B, n, Hv, dv), 7.0, dtype=torch.bfloat16, device=DEV)
+    o2 = o1.clone()
+    f.step(*a, big, slots=slots, accepted=acc, out=o1)
+    for i in range(0, B, 10):
+        f.step(*[t[i:i + 10] for t in a], small, slots=slots[i:i + 10], accepted=acc[i:i + 10], out=o2[i:i + 10])
+    assert torch.equal(o1, o2) and torch.equal(big, small) and f.status() == lm.LING_MOE_OK
+    assert (o1[[0, 5, 37, 129]] == 7).all() and not torch.equal(big, st)
+    x = sub([t[77] for t in a], slice(0, n))
+    s0 = np64(st[slots[77]])
+    want, states = D.rule(*x, s0, dk**-0.5)
+    eo, es = D.step_bound(*x, s0, dk**-0.5)
+    close_out(np64(o1[77]), want, eo)
+    if acc[77]:
+        close_state(np64(big[slots[77]]), states[acc[77] - 1], es[acc[77] - 1])
+    assert torch.equal(f.step(*a, st.clone(), slots=slots, accepted=acc, out=o2), o1)
+    f.test_set_wait(True, 2_000_000)  # the copies of later heads are not issued: the waits run out
+    f.step(*a, st.clone(), slots=slots)
+    assert f.status() == lm.LING_MOE_ERR_DEVICE_TIMEOUT
+    f.test_set_wait(False)
+    f.step(*a, small.copy_(st), slots=slots, accepted=acc, out=o2)
+    assert torch.equal(o1, o2) and torch.equal(big, small) and f.status() == lm.LING_MOE_OK
+    f.close()

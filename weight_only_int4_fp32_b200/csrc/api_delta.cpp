@@ -27,7 +27,7 @@ Span span(const void* p, size_t es, const int64_t n[4], const int64_t st[4]) {
 }  // namespace
 
 struct ling_moe_delta {
-  int device = 0;
+  int device = 0, sms = 0;
   ling_moe_delta_config_t cfg{};
   int seg_chunks = 0;
   unsigned char* ws = nullptr;
@@ -126,6 +126,7 @@ int ling_moe_delta_create(const ling_moe_delta_config_t* cfg, ling_moe_delta_t**
   ling_moe_delta* h = new (std::nothrow) ling_moe_delta();
   if (!h) return fail_arg(LING_MOE_ERR_OOM, "host allocation failed");
   h->device = dev;
+  h->sms = sms;
   h->cfg = *cfg;
   if (h->cfg.scale == 0.f) h->cfg.scale = 1.f / std::sqrt((float)cfg->head_k);
   const int64_t need = chunks_bound(cfg->max_tokens, cfg->max_seqs);
@@ -159,7 +160,7 @@ int ling_moe_delta_step(ling_moe_delta_t* h, const ling_moe_delta_io_t* io, int 
   if (int rc = fill(h, io, seqs, tokens, &p)) return rc;
   p.nseq = seqs;
   p.accepted = accepted;
-  cudaError_t e = launch_delta_step(p, h->cfg.head_k, static_cast<cudaStream_t>(stream));
+  cudaError_t e = launch_delta_step(p, h->cfg.head_k, h->sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail_cuda(e, "delta rule step launch");
   h->launches.fetch_add(1);
   return LING_MOE_OK;

@@ -153,6 +153,28 @@ __device__ __forceinline__ void load_decay(const float* src, int per_channel, bo
     for (int i = 0; i < N; ++i) x[i] = src[i];
   }
 }
+// two floats in one register pair, and the same operation on both
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pack2(float x, float y) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
 // exp(g), 1 for g > 0; a NaN stays one
 __device__ __forceinline__ float decay_of(float g) { return expf(g > 0.f ? 0.f : g); }
 
@@ -174,107 +196,220 @@ __device__ __forceinline__ float transpose_sum32(float v[32]) {
 }  // namespace
 
 // ---------------------------------------------------------------- step
-// A CTA takes 32 columns of one head's state: thread (rg, cl) = (tid / 8,
-// tid % 8) holds columns 4 cl.. of rows rg, rg + 16, ...  Both products with
-// the decayed state, S^T k and S^T q, are formed together and
-// S_new^T q = S^T q + (k . q) u, so a token costs one exchange between the
-// warps.
+// A warp takes 16 columns of one head's state and all of its rows: lane (rg, cl)
+// = (lane / 4, lane % 4) holds columns 4 cl.. of rows rg R .. + R - 1 in
+// registers, so that no token needs more than its own warp.  Both products with
+// the decayed state, S^T k and S^T q, are formed together, and S_new^T q =
+// S^T q + (k . q) u.  The warps of a CTA share the tokens' unit keys and
+// queries and their decays, which a warp per token prepares while the state is
+// on its way from HBM.
+constexpr int kStepCols = 16;  // state columns of a warp
+// the place of channel c among a token's channels: R of them per row group, padded so
+// that the eight row groups' 16-byte reads fall into different banks
 template <int DK>
-__global__ void __launch_bounds__(128) delta_step_kernel(const DeltaParams p) {
-  constexpr int R = DK / 16, CPL = DK / 32;
-  __shared__ float sk[kDeltaMaxStep][DK], sq[kDeltaMaxStep][DK], sa[kDeltaMaxStep][DK];
-  __shared__ float sv[kDeltaMaxStep][kDeltaCols], sb[kDeltaMaxStep], skq[kDeltaMaxStep];
-  __shared__ float4 red[2][4][2][8];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int splits = p.dv / kDeltaCols;
-  const int split = blockIdx.x % splits, h = blockIdx.x / splits % p.Hv, b = blockIdx.x / splits / p.Hv;
-  const int slot = slot_of(p, b);
-  if (slot < 0) return;
-  const int cl = tid & 7, rg = tid >> 3;
-  const int col0 = split * kDeltaCols;
-  float* sp = p.state + ((size_t)slot * p.Hv + h) * DK * p.dv + (size_t)rg * p.dv + col0 + 4 * cl;
-  float4 S[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) S[r] = *reinterpret_cast<const float4*>(sp + (size_t)16 * r * p.dv);
+__host__ __device__ constexpr int step_at(int c) { return c + 4 * (c / (DK / 8)); }
 
-  const int n = p.T, hk = h / (p.Hv / p.Hk);
-  for (int t = warp; t < n; t += 4) {
-    float q[CPL], k[CPL], g[CPL];
+template <int DK>
+struct StepTokens {  // a head's tokens, prepared
+  float k[kDeltaMaxStep][DK + 32], q[kDeltaMaxStep][DK + 32], a[kDeltaMaxStep][DK + 32];
+  float v[kDeltaMaxStep][128];
+  float beta[kDeltaMaxStep], kq[kDeltaMaxStep];
+};
+// what a lane loads of a token: CPL channels each of q, k and g, two or four of v
+template <int DK>
+struct StepRaw {
+  float q[DK / 32], k[DK / 32], g[DK / 32], v[4], beta;
+  __device__ __forceinline__ void load(const DeltaParams& p, int b, int h, int t, int lane) {
+    constexpr int CPL = DK / 32;
+    const int hk = h / (p.Hv / p.Hk);
     load_bf16<CPL>(p.q + b * p.q_b + t * p.q_t + hk * p.q_h + CPL * lane, p.vec_qk, q);
     load_bf16<CPL>(p.k + b * p.k_b + t * p.k_t + hk * p.k_h + CPL * lane, p.vec_qk, k);
     load_decay<CPL>(p.g + b * p.g_b + t * p.g_t + h * p.g_h + p.g_c * CPL * lane, p.g_c, p.vec_g, g);
+    const __nv_bfloat16* vp = p.v + b * p.v_b + t * p.v_t + h * p.v_h + 2 * lane;
+    load_bf16<2>(vp, p.vec_v, v);
+    if (p.dv > 64) load_bf16<2>(vp + 64, p.vec_v, v + 2);
+    beta = p.beta[b * p.be_b + t * p.be_t + h * p.be_h];
+  }
+  __device__ __forceinline__ void finish(StepTokens<DK>& s, int t, int lane) {
+    *reinterpret_cast<float2*>(&s.v[t][2 * lane]) = make_float2(v[0], v[1]);
+    *reinterpret_cast<float2*>(&s.v[t][2 * lane + 64]) = make_float2(v[2], v[3]);
+    constexpr int CPL = DK / 32;
     float qq = 0.f, kk = 0.f, kq = 0.f;
 #pragma unroll
     for (int c = 0; c < CPL; ++c) qq += q[c] * q[c], kk += k[c] * k[c];
     const float rq = 1.f / sqrtf(warp_sum(qq) + kNormEps), rk = 1.f / sqrtf(warp_sum(kk) + kNormEps);
 #pragma unroll
     for (int c = 0; c < CPL; ++c) {
+      const int at = step_at<DK>(CPL * lane + c);
       q[c] *= rq;
       k[c] *= rk;
       kq += q[c] * k[c];
-      sq[t][CPL * lane + c] = q[c];
-      sk[t][CPL * lane + c] = k[c];
-      sa[t][CPL * lane + c] = decay_of(g[c]);
+      s.q[t][at] = q[c];
+      s.k[t][at] = k[c];
+      s.a[t][at] = decay_of(g[c]);
     }
     kq = warp_sum(kq);
     if (lane == 0) {
-      skq[t] = kq;
-      sb[t] = p.beta[b * p.be_b + t * p.be_t + h * p.be_h];
+      s.kq[t] = kq;
+      s.beta[t] = beta;
     }
-    sv[t][lane] = __bfloat162float(p.v[b * p.v_b + t * p.v_t + h * p.v_h + col0 + lane]);
   }
-  const int commit = p.accepted ? clamp_int(p.accepted[b], 0, n) : n;
-  __syncthreads();
+};
+template <int DK>
+__host__ __device__ constexpr int step_smem(int dv, bool ahead) {
+  return (ahead ? 2 * (int)sizeof(StepTokens<DK>) + DK * dv * 4 : (int)sizeof(StepTokens<DK>)) + 16;
+}
+
+// AHEAD: a CTA takes whole heads, blockIdx.x, + gridDim.x, ...; while it
+// computes one, a bulk copy brings the next one's state to shared memory and
+// its tokens come to registers.  Otherwise one item (a head or a part of its
+// columns) per CTA.
+template <int DK, bool AHEAD>
+__global__ void __launch_bounds__(256, 2) delta_step_kernel(const DeltaParams p) {
+  constexpr int R = DK / 8;
+  extern __shared__ __align__(128) unsigned char dsm[];
+  float* sstate = reinterpret_cast<float*>(dsm);
+  StepTokens<DK>* tok = reinterpret_cast<StepTokens<DK>*>(dsm + (AHEAD ? DK * p.dv * 4 : 0));
+  uint64_t* bar = reinterpret_cast<uint64_t*>(tok + (AHEAD ? 2 : 1));
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int splits = AHEAD ? 1 : p.dv / (kStepCols * warps);
+  const int items = AHEAD ? p.nseq * p.Hv : (int)gridDim.x;
+  const int cl = lane & 3, rg = lane >> 2;
+  const int n = p.T;
+  int item = blockIdx.x;
+  // the next item at or after `i` that has a slot
+  auto find = [&](int i) {
+    if constexpr (AHEAD)
+      while (i < items && slot_of(p, i / p.Hv) < 0) i += gridDim.x;
+    return i;
+  };
+  item = find(item);
+  if (item >= items) return;
+  int split = item % splits, h = item / splits % p.Hv, b = item / splits / p.Hv, slot = slot_of(p, b);
+  if (slot < 0) return;
+  const int col = (split * warps + warp) * kStepCols + 4 * cl;
+  const size_t off = (size_t)rg * R * p.dv + col;  // this lane's first element of a head's state
+  if (AHEAD && threadIdx.x == 0) {
+    mbar_init(bar, 1);
+    fence_mbar_init();
+  }
+  f2 S[R / 2][4];  // rows 2 r, 2 r + 1 of each column
+  auto take = [&](const float* sp) {
+#pragma unroll
+    for (int r = 0; r < R; r += 2) {
+      const float4 x = *reinterpret_cast<const float4*>(sp + (size_t)r * p.dv);
+      const float4 y = *reinterpret_cast<const float4*>(sp + (size_t)(r + 1) * p.dv);
+      S[r / 2][0] = pack2(x.x, y.x), S[r / 2][1] = pack2(x.y, y.y), S[r / 2][2] = pack2(x.z, y.z), S[r / 2][3] = pack2(x.w, y.w);
+    }
+  };
+  take(p.state + ((size_t)slot * p.Hv + h) * DK * p.dv + off);
+  for (int t = warp; t < n; t += warps) {
+    StepRaw<DK> raw;
+    raw.load(p, b, h, t, lane);
+    raw.finish(tok[0], t, lane);
+  }
+  bool dead = false;  // a wait ran out: the results are void
+  uint32_t phase = 0;
+  for (int turn = 0;; turn ^= 1) {
+    __syncthreads();  // the item's tokens are prepared, its state is out of shared memory
+    const StepTokens<DK>& s = tok[AHEAD ? turn : 0];
+    int next = items, nh = 0, nb = 0, nslot = 0;
+    StepRaw<DK> raw;
+    if constexpr (AHEAD) {
+      next = find(item + gridDim.x);
+      if (next < items) {
+        nh = next % p.Hv, nb = next / p.Hv, nslot = slot_of(p, nb);
+        if (threadIdx.x == 0) {
+          mbar_arrive_expect_tx(bar, DK * p.dv * 4);
+          if (!p.skip) bulk_g2s(sstate, p.state + ((size_t)nslot * p.Hv + nh) * DK * p.dv, DK * p.dv * 4, bar);
+        }
+        if (warp < n) raw.load(p, nb, nh, warp, lane);
+      }
+    }
+    const int commit = p.accepted ? clamp_int(p.accepted[b], 0, n) : n;
+    __nv_bfloat16* op = p.out + ((size_t)b * n * p.Hv + h) * p.dv + col;
+    float* sp = p.state + ((size_t)slot * p.Hv + h) * DK * p.dv + off;
 #pragma unroll 1
-  for (int t = 0; t < n; ++t) {
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+    for (int t = 0; t < n; ++t) {
+      f2 w[8];  // S^T k of the four columns, then S^T q; even and odd rows apart
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int row = rg + 16 * r;
-      const float a = sa[t][row], k = sk[t][row], q = sq[t][row];
-      S[r].x *= a, S[r].y *= a, S[r].z *= a, S[r].w *= a;
-      x.x = fmaf(S[r].x, k, x.x), x.y = fmaf(S[r].y, k, x.y), x.z = fmaf(S[r].z, k, x.z), x.w = fmaf(S[r].w, k, x.w);
-      y.x = fmaf(S[r].x, q, y.x), y.y = fmaf(S[r].y, q, y.y), y.z = fmaf(S[r].z, q, y.z), y.w = fmaf(S[r].w, q, y.w);
-    }
+      for (int i = 0; i < 8; ++i) w[i] = 0ull;
 #pragma unroll
-    for (int o = 8; o <= 16; o <<= 1) {
-      x.x += __shfl_xor_sync(0xffffffffu, x.x, o), x.y += __shfl_xor_sync(0xffffffffu, x.y, o);
-      x.z += __shfl_xor_sync(0xffffffffu, x.z, o), x.w += __shfl_xor_sync(0xffffffffu, x.w, o);
-      y.x += __shfl_xor_sync(0xffffffffu, y.x, o), y.y += __shfl_xor_sync(0xffffffffu, y.y, o);
-      y.z += __shfl_xor_sync(0xffffffffu, y.z, o), y.w += __shfl_xor_sync(0xffffffffu, y.w, o);
-    }
-    if (lane < 8) {
-      red[t & 1][warp][0][lane] = x;
-      red[t & 1][warp][1][lane] = y;
-    }
-    __syncthreads();
-    x = red[t & 1][0][0][cl], y = red[t & 1][0][1][cl];
+      for (int r = 0; r < R; r += 4) {
+        const int at = step_at<DK>(R) * rg + r;
+        const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(&s.a[t][at]);
+        const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(&s.k[t][at]);
+        const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(&s.q[t][at]);
 #pragma unroll
-    for (int w = 1; w < 4; ++w) {
-      const float4 a = red[t & 1][w][0][cl], c = red[t & 1][w][1][cl];
-      x.x += a.x, x.y += a.y, x.z += a.z, x.w += a.w;
-      y.x += c.x, y.y += c.y, y.z += c.z, y.w += c.w;
-    }
-    const float4 v = *reinterpret_cast<const float4*>(&sv[t][4 * cl]);
-    const float beta = sb[t], kq = skq[t];
-    const float4 u = make_float4(beta * (v.x - x.x), beta * (v.y - x.y), beta * (v.z - x.z), beta * (v.w - x.w));
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const float k = sk[t][rg + 16 * r];
-      S[r].x = fmaf(k, u.x, S[r].x), S[r].y = fmaf(k, u.y, S[r].y);
-      S[r].z = fmaf(k, u.z, S[r].z), S[r].w = fmaf(k, u.w, S[r].w);
-    }
-    if (rg == 0) {
-      __nv_bfloat162 o[2] = {
-          __floats2bfloat162_rn(p.scale * fmaf(kq, u.x, y.x), p.scale * fmaf(kq, u.y, y.y)),
-          __floats2bfloat162_rn(p.scale * fmaf(kq, u.z, y.z), p.scale * fmaf(kq, u.w, y.w))};
-      *reinterpret_cast<uint2*>(p.out + (((size_t)b * n + t) * p.Hv + h) * p.dv + col0 + 4 * cl) =
-          *reinterpret_cast<const uint2*>(o);
-    }
-    if (t + 1 == commit) {
+          for (int c = 0; c < 4; ++c) {
+            f2& x = S[r / 2 + i][c];
+            x = mul2(x, i ? a.y : a.x);
+            w[c] = fma2(x, i ? k.y : k.x, w[c]);
+            w[4 + c] = fma2(x, i ? q.y : q.x, w[4 + c]);
+          }
+      }
+      float z[8];
 #pragma unroll
-      for (int r = 0; r < R; ++r) *reinterpret_cast<float4*>(sp + (size_t)16 * r * p.dv) = S[r];
+      for (int i = 0; i < 8; ++i) {
+        const float2 x = unpack2(w[i]);
+        z[i] = x.x + x.y;
+      }
+      // the sums over the row groups: lane (rg, cl) is left with the sum of z[rg]
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) {
+        const bool up = rg & o;
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+          const float keep = up ? z[i + o] : z[i], send = up ? z[i] : z[i + o];
+          z[i] = keep + __shfl_xor_sync(0xffffffffu, send, 4 * o);
+        }
+      }
+      const float beta = s.beta[t];
+      const float4 v4 = *reinterpret_cast<const float4*>(&s.v[t][col]);
+      const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+      float u[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = beta * (v[i] - __shfl_sync(0xffffffffu, z[0], 4 * i + cl));
+#pragma unroll
+      for (int r = 0; r < R; r += 4) {
+        const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(&s.k[t][step_at<DK>(R) * rg + r]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) S[r / 2 + i][c] = fma2(i ? k.y : k.x, pack2(u[c], u[c]), S[r / 2 + i][c]);
+      }
+      if (rg >= 4) {  // S^T q of column rg - 4
+        const float ui = rg == 4 ? u[0] : rg == 5 ? u[1] : rg == 6 ? u[2] : u[3];
+        op[(size_t)t * p.Hv * p.dv + rg - 4] = __float2bfloat16_rn(p.scale * fmaf(s.kq[t], ui, z[0]));
+      }
+      if (t + 1 == commit) {
+#pragma unroll
+        for (int r = 0; r < R; r += 2) {
+          float2 x[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) x[c] = unpack2(S[r / 2][c]);
+          *reinterpret_cast<float4*>(sp + (size_t)r * p.dv) = make_float4(x[0].x, x[1].x, x[2].x, x[3].x);
+          *reinterpret_cast<float4*>(sp + (size_t)(r + 1) * p.dv) = make_float4(x[0].y, x[1].y, x[2].y, x[3].y);
+        }
+      }
     }
+    if (!AHEAD || next >= items) break;
+    if (warp < n) raw.finish(tok[turn ^ 1], warp, lane);
+    for (int t = warp + warps; t < n; t += warps) {
+      raw.load(p, nb, nh, t, lane);
+      raw.finish(tok[turn ^ 1], t, lane);
+    }
+    if (!dead) dead = !mbar_wait(bar, phase, p.wait_ns, p.err);
+    dead = __syncthreads_or(dead);
+    if (dead) {  // a copy that is late must have landed before the CTA ends
+      if (threadIdx.x == 0 && !p.skip) mbar_wait(bar, phase, kLandNs, p.err);
+      return;
+    }
+    phase ^= 1;
+    item = next, h = nh, b = nb, slot = nslot;
+    take(sstate + off);
   }
 }
 
@@ -990,6 +1125,9 @@ static cudaError_t setup_dk() {
   cudaError_t e = cudaFuncSetAttribute(delta_prep_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        PrepCfg<DK>::kSmem);
   if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(delta_step_kernel<DK, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             step_smem<DK>(128, true));
+  if (e == cudaSuccess)
     e = cudaFuncSetAttribute(delta_scan_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, ScanCfg<DK>::kSmem);
   return e;
 }
@@ -998,12 +1136,30 @@ cudaError_t setup_delta() {
   return e != cudaSuccess ? e : setup_dk<128>();
 }
 
-cudaError_t launch_delta_step(const DeltaParams& p, int dk, cudaStream_t s) {
-  const unsigned grid = (unsigned)p.nseq * p.Hv * (p.dv / kDeltaCols);
+template <int DK, bool AHEAD>
+static void step_launch(const DeltaParams& p, unsigned grid, int warps, cudaStream_t s) {
+  delta_step_kernel<DK, AHEAD><<<grid, 32 * warps, step_smem<DK>(p.dv, AHEAD), s>>>(p);
+}
+// More heads than CTAs fit at once: whole heads with the next one's state on its
+// way.  Otherwise one item per CTA, a part of a head's columns where whole heads
+// would leave SMs without work.
+cudaError_t launch_delta_step(const DeltaParams& p, int dk, int sms, cudaStream_t s) {
+  const long long heads = (long long)p.nseq * p.Hv;
+  int warps = p.dv / kStepCols;
+  const int fit = sms * 16 / warps;  // 16 warps per SM (registers)
+  if (heads > fit) {
+    if (dk == 64)
+      step_launch<64, true>(p, (unsigned)fit, warps, s);
+    else
+      step_launch<128, true>(p, (unsigned)fit, warps, s);
+    return cudaGetLastError();
+  }
+  while (warps > 2 && heads * (p.dv / kStepCols / warps) < 2ll * sms) warps /= 2;
+  const unsigned grid = (unsigned)(heads * (p.dv / kStepCols / warps));
   if (dk == 64)
-    delta_step_kernel<64><<<grid, 128, 0, s>>>(p);
+    step_launch<64, false>(p, grid, warps, s);
   else
-    delta_step_kernel<128><<<grid, 128, 0, s>>>(p);
+    step_launch<128, false>(p, grid, warps, s);
   return cudaGetLastError();
 }
 cudaError_t launch_delta_prep(const DeltaParams& p, int dk, cudaStream_t s) {
