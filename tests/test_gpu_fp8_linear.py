@@ -174,3 +174,37 @@ def test_refusals_and_wait_timeout():
     f.test_set_wait(-1)
     assert torch.equal(f.forward(x), y) and f.status() == lm.LING_MOE_OK
     f.close()
+
+
+def test_long_rows_take_the_separate_quantisation():
+    """K = 13100: eight tokens' codes no longer fit a CTA's shared memory; seven and fewer do."""
+    N, K = 40, 13100
+    codes, scales = weights(N, K, 11)
+    f = lm.BlockFP8Linear(codes, scales, max_tokens=8)
+    for T, launches in ((8, 2), (7, 1), (1, 1)):
+        n = f.launch_count()
+        x = tokens(T, K, T)
+        check(f.forward(x, out_dtype=torch.float32), x, codes, scales)
+        check(f.forward(x, out_dtype=torch.float32), x, codes, scales)
+        assert f.launch_count() == n + 2 * launches
+    f.close()
+
+
+@pytest.mark.parametrize("T", [1, 8, 40])
+def test_token_codes_at_the_borders_between_codes(T):
+    """Weights are the identity, so outputs show the codes: quotients on, and a step beside, the borders."""
+    N = K = 128
+    codes = torch.eye(N, device=DEV).to(torch.float8_e4m3fn)
+    f = lm.BlockFP8Linear(codes, torch.ones(1, 1, device=DEV), max_tokens=T)
+    mids = torch.tensor([m * 2.0**e for e in range(-11, 5) for m in (17, 19, 21, 23, 25, 27, 29)])[:110]
+    for top in (448.0, 447.0, 450.0, 3.0, 1e-3, 2.0**-100, 2.0**-120):
+        x = torch.zeros(T, K)
+        x[:, 1:111] = (mids * (top / 448.0)).bfloat16().float()
+        x[:, 0] = top
+        x = x.bfloat16().to(DEV)
+        y = f.forward(x, out_dtype=torch.float32)
+        c, s = F.quantize_tokens(x.float().cpu().numpy())
+        want = F.e4m3_decode(c) * s.astype(np.float64)
+        # one product of a code with the scale, rounded once; below 2^-126 it may flush
+        assert (np.abs(y.double().cpu().numpy() - want) <= U * np.abs(want) + 2.0**-126).all()
+    f.close()

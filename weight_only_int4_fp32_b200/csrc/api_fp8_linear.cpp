@@ -104,12 +104,18 @@ int ling_moe_fp8_linear_forward(ling_moe_fp8_linear_t* h, const void* x, int64_t
     return fail_arg(LING_MOE_ERR_INVALID_ARG, "out overlaps x");
   if (int rc = check_same_device(h->device)) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream_v);
-  cudaError_t e = launch_f8_quantize(static_cast<const __nv_bfloat16*>(x), x_stride, T, h->K, h->kb, h->tpad, h->xq,
-                                     h->sx, s);
+  const bool fused = T <= kF8GemvMaxT && f8_gemv_smem(T, h->kb) <= kF8GemvSmem;
+  cudaError_t e = cudaSuccess;
+  if (!fused)
+    e = launch_f8_quantize(static_cast<const __nv_bfloat16*>(x), x_stride, T, h->K, h->kb, h->tpad, h->xq, h->sx, s);
   if (e != cudaSuccess) return fail_cuda(e, "token quantisation launch");
   F8Params p{};
   p.w = h->w;
   p.sw = h->sw;
+  p.x = static_cast<const __nv_bfloat16*>(x);
+  p.x_stride = x_stride;
+  p.K = h->K;
+  p.x_vec = is_aligned(x, 16) && (T == 1 || x_stride % 8 == 0);
   p.xq = h->xq;
   p.sx = h->sx;
   p.out = out;
@@ -124,7 +130,7 @@ int ling_moe_fp8_linear_forward(ling_moe_fp8_linear_t* h, const void* x, int64_t
   p.wait_ns = h->wait_ns;
   p.skip_cta = h->skip_cta;
   if (T <= kF8GemvMaxT) {
-    e = launch_f8_gemv(p, s);
+    e = launch_f8_gemv(p, h->sms, fused, s);
   } else {
     // the tile width whose waves of tiles cost least: a tile's K loop costs
     // about its width, plus a fixed part worth some 48 columns
@@ -144,7 +150,7 @@ int ling_moe_fp8_linear_forward(ling_moe_fp8_linear_t* h, const void* x, int64_t
     e = launch_f8_gemm(h->maps, p, tile, (int)(tiles < h->sms ? tiles : h->sms), s);
   }
   if (e != cudaSuccess) return fail_cuda(e, "linear launch");
-  h->launches.fetch_add(2);
+  h->launches.fetch_add(fused ? 1 : 2);
   return LING_MOE_OK;
 }
 

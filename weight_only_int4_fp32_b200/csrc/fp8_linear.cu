@@ -11,15 +11,16 @@
 // to an fp32 accumulator outside the tensor cores, since both scales change
 // with every 128 inputs.  One rounding to the output type at the end.
 //
-// Two kernels follow the quantisation, launched as its programmatic
-// dependent (their set-up and first weight loads overlap it):
+// Two kernels:
 //  * up to 8 tokens: weights streamed from HBM straight into mma.sync
-//    fragments (e4m3 -> fp16 exactly), 16 outputs per CTA, the blocks of K
-//    dealt to its 8 warps.  Bound: HBM, N x K bytes.
+//    fragments (e4m3 -> fp16 exactly), 16 outputs at a time per CTA, the blocks
+//    of K dealt to its 8 warps, tokens quantised in the same launch.  Bound:
+//    HBM, N x K bytes.
 //  * more: tcgen05 (kind::f8f6f4) tiles of 128 tokens x 32..256 outputs.  Each
 //    128-wide K block is one pipeline stage and one chain of four MMAs into
-//    one of two TMEM buffers; 8 warps read a finished buffer, scale it and
+//    one of two TMEM buffers; 16 warps read a finished buffer, scale it and
 //    add it to accumulators in registers while the next block multiplies.
+//    A quantisation kernel runs first, the tiles as its programmatic dependent.
 //    Bound: tensor cores for many tokens, HBM for few.
 // Source of the format: vLLM recipe page "inclusionAI/Ling-3.0-flash", section
 // Overview (the block-FP8 checkpoint); the page does not define it, the
@@ -50,9 +51,56 @@ __device__ __forceinline__ uint32_t f8x2_to_f16x2(uint32_t pair) {
 }
 
 // ---------------------------------------------------------------- quantisation
-// 16 lanes take one token's 128 inputs of block blockIdx.y, 8 each; a CTA
-// takes 64 tokens.  HBM bound for many tokens (2 bytes read, 1 written).
-constexpr int kQTokens = 64;
+// 16 lanes take one token's 128 inputs of one block, 8 each.
+
+// codes of x / s for 8 values.  The quotient's rounding matters only where a
+// border between two codes lies within it: x times the rounded 1 / s is within
+// 3 2^-24 of the rounded quotient, so where both ends of 2^-21 around it give
+// the same code that is the answer; otherwise, and where 1 / s may overflow,
+// the division decides.
+__device__ __forceinline__ uint2 f8_codes(const uint32_t r[4], float s) {
+  const float inv = __frcp_rn(s);
+  bool sure = s > 1e-30f;
+  uint32_t c[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float x = __fmul_rn(bf16lo(r[e]), inv), y = __fmul_rn(bf16hi(r[e]), inv);
+    c[e] = f8x2(fmaf(x, 0x1p-21f, x), fmaf(y, 0x1p-21f, y));
+    sure &= c[e] == f8x2(fmaf(x, -0x1p-21f, x), fmaf(y, -0x1p-21f, y));
+  }
+  if (!sure) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c[e] = f8x2(__fdiv_rn(bf16lo(r[e]), s), __fdiv_rn(bf16hi(r[e]), s));
+  }
+  return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+}
+// 8 inputs k .. of a row, zeros at and past K
+__device__ __forceinline__ void load8(const __nv_bfloat16* src, int k, int K, int vec, uint32_t r[4]) {
+  r[0] = r[1] = r[2] = r[3] = 0u;
+  if (vec && k + 8 <= K) {
+    const uint4 v = *reinterpret_cast<const uint4*>(src);
+    r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (k + e < K) r[e >> 1] |= (uint32_t) * reinterpret_cast<const unsigned short*>(src + e) << (16 * (e & 1));
+  }
+}
+// the block's scale, from the 16 lanes that hold it (all 16 take part)
+__device__ __forceinline__ float block_scale16(const uint32_t r[4]) {
+  float a = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) a = fmaxf(a, fmaxf(fabsf(bf16lo(r[e])), fabsf(bf16hi(r[e]))));
+  const unsigned int half = 0xFFFFu << (threadIdx.x & 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(half, a, o));
+  return a > 0.f ? __fmul_rn(a, 1.0f / 448.0f) : 1.0f;
+}
+
+// A kernel of its own in front of the tensor-core tiles: 16 groups of 16 lanes,
+// kQIter tokens each, whose loads are in flight together.  HBM bound for many
+// tokens (2 bytes read, 1 written per input).
+constexpr int kQIter = 2, kQTokens = 16 * kQIter;
 
 __global__ void __launch_bounds__(256) f8_quantize_kernel(const __nv_bfloat16* __restrict__ x, long long stride, int T,
                                                           int K, int kb, int tpad, int vec, uint8_t* __restrict__ xq,
@@ -60,113 +108,188 @@ __global__ void __launch_bounds__(256) f8_quantize_kernel(const __nv_bfloat16* _
   pdl_launch_dependents();
   const int b = blockIdx.y, l = threadIdx.x & 15;
   const int k = b * kF8Block + 8 * l;
-  for (int i = threadIdx.x >> 4; i < kQTokens; i += 16) {
-    const long long t = (long long)blockIdx.x * kQTokens + i;
-    if (t >= T) break;  // both halves of a warp: only whole 16-lane groups shuffle below
-    const __nv_bfloat16* src = x + t * stride + k;
-    uint32_t r[4] = {0u, 0u, 0u, 0u};
-    if (vec && k + 8 <= K) {
-      const uint4 v = *reinterpret_cast<const uint4*>(src);
-      r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
-    } else {
+  const int t0 = blockIdx.x * kQTokens + (threadIdx.x >> 4);
+  uint32_t r[kQIter][4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (k + e < K) r[e >> 1] |= (uint32_t) * reinterpret_cast<const unsigned short*>(src + e) << (16 * (e & 1));
-    }
-    float a = 0.f;
+  for (int i = 0; i < kQIter; ++i)
+    if (t0 + 16 * i < T) load8(x + (t0 + 16 * i) * stride + k, k, K, vec, r[i]);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) a = fmaxf(a, fmaxf(fabsf(bf16lo(r[e])), fabsf(bf16hi(r[e]))));
-    const unsigned int half = 0xFFFFu << (threadIdx.x & 16);
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(half, a, o));
-    const float s = a > 0.f ? __fmul_rn(a, 1.0f / 448.0f) : 1.0f;
-    uint32_t c[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) c[e] = f8x2(__fdiv_rn(bf16lo(r[e]), s), __fdiv_rn(bf16hi(r[e]), s));
-    *reinterpret_cast<uint2*>(xq + t * ((long long)kb * kF8Block) + k) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+  for (int i = 0; i < kQIter; ++i) {
+    const long long t = t0 + 16 * i;
+    if (t >= T) break;  // whole 16-lane groups: only they shuffle together
+    const float s = block_scale16(r[i]);
+    *reinterpret_cast<uint2*>(xq + t * ((long long)kb * kF8Block) + k) = f8_codes(r[i], s);
     if (l == 0) sx[(long long)b * tpad + t] = s;
   }
 }
 
 // ---------------------------------------------------------------- 1..8 tokens
-// A warp's share of K: blocks w, w + 8, ...; kU of them are in flight at once
-// (4 x 16 bytes per lane each).  Lane (g, c) = (lane / 4, lane % 4) loads codes
-// 16 c .. + 15 of each half block of rows g and g + 8; the K order inside the
-// MMAs is a permutation of the 64 codes, the same for weights and tokens.
+// A CTA takes groups of 16 outputs, grid strided, and deals the blocks of K to
+// its 8 warps: w, w + 8, ...; a warp keeps kU of them in flight (4 x 16 bytes
+// per lane each), each replaced as soon as it is used, across groups too.  Lane
+// (g, c) = (lane / 4, lane % 4) loads codes 16 c .. + 15 of each half block of
+// rows g and g + 8; the K order inside the MMAs is a permutation of the 64
+// codes, the same for weights and tokens.
+//
+// The CTAs of a cluster (one, or four where there is much to do) quantise the
+// tokens into the shared memory of each while their first weights are on their
+// way: one launch.  Where the tokens' codes do not fit there (FUSED false), the
+// kernel above has left them in global memory.
 constexpr int kGemvRows = 16, kGemvWarps = 8, kU = 4;
 
-__global__ void __launch_bounds__(kGemvWarps * 32) f8_gemv_kernel(const F8Params p) {
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_ctas() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// the shared memory of CTA `rank` of the cluster, at this CTA's address
+__device__ __forceinline__ uint32_t cluster_map(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+
+template <bool FUSED>
+__global__ void __launch_bounds__(kGemvWarps * 32, 2) f8_gemv_kernel(const F8Params p) {
   __shared__ float red[kGemvWarps][32][4];
+  extern __shared__ __align__(16) unsigned char gsm[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
-  const int row0 = blockIdx.x * kGemvRows;
+  if constexpr (FUSED) cluster_arrive();
+  const int groups = (p.N + kGemvRows - 1) / kGemvRows;
   const size_t pitch = (size_t)p.kb * kF8Block;
-  const uint8_t* wa = p.w + (size_t)(row0 + g) * pitch + 16 * c;  // the padded rows exist
-  const uint8_t* wb = wa + 8 * pitch;
-  const uint8_t* xr = p.xq + (size_t)g * pitch + 16 * c;          // rows >= T: any codes, results dropped
-  const float* sw = p.sw + (size_t)(row0 / kF8Block) * p.kb;
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  bool waited = false;
-  for (int b0 = warp; b0 < p.kb; b0 += kGemvWarps * kU) {
-    uint4 a[kU][2], b[kU][2];
+  const uint8_t* wr = p.w + (size_t)g * pitch + 16 * c;  // the padded rows exist
+  uint4 a[kU][2], b[kU][2];
+  auto load = [&](int u, int grp, int kb) {
+    if (grp >= groups || kb >= p.kb) return;
+    const uint8_t* wa = wr + (size_t)grp * kGemvRows * pitch + (size_t)kb * kF8Block;
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int kb = b0 + kGemvWarps * u;
-      if (kb < p.kb) {
+    for (int h = 0; h < 2; ++h) {
+      a[u][h] = ldg_stream(wa + 64 * h);
+      b[u][h] = ldg_stream(wa + 8 * pitch + 64 * h);
+    }
+  };
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          a[u][h] = ldg_stream(wa + (size_t)kb * kF8Block + 64 * h);
-          b[u][h] = ldg_stream(wb + (size_t)kb * kF8Block + 64 * h);
+  for (int u = 0; u < kU; ++u) load(u, blockIdx.x, warp + kGemvWarps * u);
+
+  // the tokens: row pitch in bytes (half a bank row off a multiple of 128), scales [kb][T]
+  const int row = (int)pitch + 64;
+  float* ssx = reinterpret_cast<float*>(gsm + (size_t)p.T * row);
+  const int tg = min(g, p.T - 1), t0 = min(2 * c, p.T - 1), t1 = min(2 * c + 1, p.T - 1);  // past T: results dropped
+  if constexpr (FUSED) {
+    const int l = threadIdx.x & 15, pairs = p.T * p.kb;
+    const int ctas = (int)cluster_ctas(), step = 16 * ctas;
+    constexpr int kQ = 4;
+    int i = (threadIdx.x >> 4) + 16 * (int)cluster_rank(), t = i / p.kb, kb = i - t * p.kb;  // token and block of a pair
+    const int dt = step / p.kb, dkb = step - dt * p.kb;
+    cluster_wait();  // every CTA of the cluster runs
+    while (i < pairs) {
+      uint32_t r[kQ][4];
+      int at[kQ], as[kQ];
+#pragma unroll
+      for (int q = 0; q < kQ; ++q) {
+        at[q] = -1;
+        if (i < pairs) {
+          load8(p.x + t * p.x_stride + kb * kF8Block + 8 * l, kb * kF8Block + 8 * l, p.K, p.x_vec, r[q]);
+          at[q] = t * row + kb * kF8Block + 8 * l;
+          as[q] = p.T * row + 4 * (kb * p.T + t);
+        }
+        i += step, t += dt, kb += dkb;
+        if (kb >= p.kb) kb -= p.kb, ++t;
+      }
+#pragma unroll
+      for (int q = 0; q < kQ; ++q) {
+        if (at[q] < 0) break;  // whole 16-lane groups
+        const float s = block_scale16(r[q]);
+        const uint2 codes = f8_codes(r[q], s);
+        for (int k = 0; k < ctas; ++k) {
+          const uint32_t base = cluster_map(smem_u32(gsm), (uint32_t)k);
+          asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" :: "r"(base + at[q]), "r"(codes.x), "r"(codes.y)
+                       : "memory");
+          if (l == 0) asm volatile("st.shared::cluster.f32 [%0], %1;" :: "r"(base + as[q]), "f"(s) : "memory");
         }
       }
     }
-    if (!waited) {
-      pdl_wait();  // the tokens' codes
-      waited = true;
-    }
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    pdl_wait();  // the tokens' codes and scales
+  }
+  const uint8_t* xg = p.xq + (size_t)tg * pitch + 16 * c;
+  const unsigned char* xs = gsm + (size_t)tg * row + 16 * c;
+
+  for (int grp = blockIdx.x; grp < groups; grp += gridDim.x) {
+    const float* sw = p.sw + (size_t)(grp * kGemvRows / kF8Block) * p.kb;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int b0 = warp; b0 < p.kb; b0 += kGemvWarps * kU) {
+      // what follows this batch: the row's next blocks, or the next group's first
+      const bool more = b0 + kGemvWarps * kU < p.kb;
+      const int ngrp = more ? grp : grp + (int)gridDim.x, nb0 = more ? b0 + kGemvWarps * kU : warp;
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int kb = b0 + kGemvWarps * u;
-      if (kb < p.kb) {
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int u = 0; u < kU; ++u) {
+        const int kb = b0 + kGemvWarps * u;
+        if (kb < p.kb) {
+          float d[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};  // two chains of products
+          uint32_t xp[2][4], pa[2][4], pb[2][4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint4 xv = __ldcg(reinterpret_cast<const uint4*>(xr + (size_t)kb * kF8Block + 64 * h));
-          const uint32_t xp[4] = {xv.x, xv.y, xv.z, xv.w};
-          const uint32_t pa[4] = {a[u][h].x, a[u][h].y, a[u][h].z, a[u][h].w};
-          const uint32_t pb[4] = {b[u][h].x, b[u][h].y, b[u][h].z, b[u][h].w};
+          for (int h = 0; h < 2; ++h) {
+            uint4 xv;
+            if constexpr (FUSED)
+              xv = *reinterpret_cast<const uint4*>(xs + kb * kF8Block + 64 * h);
+            else
+              xv = __ldcg(reinterpret_cast<const uint4*>(xg + (size_t)kb * kF8Block + 64 * h));
+            xp[h][0] = xv.x, xp[h][1] = xv.y, xp[h][2] = xv.z, xp[h][3] = xv.w;
+            pa[h][0] = a[u][h].x, pa[h][1] = a[u][h].y, pa[h][2] = a[u][h].z, pa[h][3] = a[u][h].w;
+            pb[h][0] = b[u][h].x, pb[h][1] = b[u][h].y, pb[h][2] = b[u][h].z, pb[h][3] = b[u][h].w;
+          }
 #pragma unroll
           for (int m = 0; m < 4; ++m)
-            mma_16816(d[0], d[1], d[2], d[3], f8x2_to_f16x2(pa[m]), f8x2_to_f16x2(pb[m]), f8x2_to_f16x2(pa[m] >> 16),
-                      f8x2_to_f16x2(pb[m] >> 16), f8x2_to_f16x2(xp[m]), f8x2_to_f16x2(xp[m] >> 16), d[0], d[1], d[2],
-                      d[3]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              mma_16816(d[h][0], d[h][1], d[h][2], d[h][3], f8x2_to_f16x2(pa[h][m]), f8x2_to_f16x2(pb[h][m]),
+                        f8x2_to_f16x2(pa[h][m] >> 16), f8x2_to_f16x2(pb[h][m] >> 16), f8x2_to_f16x2(xp[h][m]),
+                        f8x2_to_f16x2(xp[h][m] >> 16), d[h][0], d[h][1], d[h][2], d[h][3]);
+          float sx0, sx1;
+          if constexpr (FUSED) {
+            sx0 = ssx[kb * p.T + t0], sx1 = ssx[kb * p.T + t1];
+          } else {
+            sx0 = __ldcg(p.sx + (size_t)kb * p.tpad + t0), sx1 = __ldcg(p.sx + (size_t)kb * p.tpad + t1);
+          }
+          const float s = __ldg(sw + kb);
+          acc[0] = fmaf(d[0][0] + d[1][0], s * sx0, acc[0]);
+          acc[1] = fmaf(d[0][1] + d[1][1], s * sx1, acc[1]);
+          acc[2] = fmaf(d[0][2] + d[1][2], s * sx0, acc[2]);
+          acc[3] = fmaf(d[0][3] + d[1][3], s * sx1, acc[3]);
         }
-        const float2 sx = __ldcg(reinterpret_cast<const float2*>(p.sx + (size_t)kb * p.tpad + 2 * c));
-        const float s = __ldg(sw + kb);
-        acc[0] = fmaf(d[0], s * sx.x, acc[0]);
-        acc[1] = fmaf(d[1], s * sx.y, acc[1]);
-        acc[2] = fmaf(d[2], s * sx.x, acc[2]);
-        acc[3] = fmaf(d[3], s * sx.y, acc[3]);
+        load(u, ngrp, nb0 + kGemvWarps * u);
       }
     }
-  }
-  *reinterpret_cast<float4*>(red[warp][lane]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-  __syncthreads();
-  // thread (token, row): consecutive threads write consecutive outputs
-  const int i = threadIdx.x;
-  if (i < 8 * kGemvRows) {
-    const int tok = i / kGemvRows, r = i % kGemvRows;
-    const int n = row0 + r;
-    if (tok < p.T && n < p.N) {
-      float s = 0.f;
+    *reinterpret_cast<float4*>(red[warp][lane]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    __syncthreads();
+    // thread (token, row): consecutive threads write consecutive outputs
+    const int i = threadIdx.x;
+    if (i < 8 * kGemvRows) {
+      const int tok = i / kGemvRows, r = i % kGemvRows;
+      const int n = grp * kGemvRows + r;
+      if (tok < p.T && n < p.N) {
+        float s = 0.f;
 #pragma unroll
-      for (int w = 0; w < kGemvWarps; ++w) s += red[w][4 * (r & 7) + (tok >> 1)][(r >> 3) * 2 + (tok & 1)];
-      const size_t at = (size_t)tok * p.out_stride + n;
-      if (p.out_bf16)
-        static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(s);
-      else
-        static_cast<float*>(p.out)[at] = s;
+        for (int w = 0; w < kGemvWarps; ++w) s += red[w][4 * (r & 7) + (tok >> 1)][(r >> 3) * 2 + (tok & 1)];
+        const size_t at = (size_t)tok * p.out_stride + n;
+        if (p.out_bf16)
+          static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(s);
+        else
+          static_cast<float*>(p.out)[at] = s;
+      }
     }
+    __syncthreads();
   }
 }
 
@@ -180,7 +303,7 @@ struct F8Cfg {
   static constexpr int kSmem = 1024 + kBarOff + 256;
   static constexpr int kTmemCols = 2 * BN;
 };
-constexpr int kF8EpiWarps = 8;
+constexpr int kF8EpiWarps = 16;
 constexpr int kF8Threads = (kF8EpiWarps + 2) * 32;
 
 __device__ __forceinline__ void tc_mma_f8(uint32_t tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -190,26 +313,55 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t tmem, uint64_t a, uint64_t b,
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, {%5, %6, %7, %8}, p;\n\t}"
       :: "r"(tmem), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(0), "r"(0), "r"(0), "r"(0));
 }
-__device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, float v[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
-        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
-      : "r"(taddr));
-}
-// waits for every load issued so far; v is what the caller uses next
-__device__ __forceinline__ void tmem_wait16(float v[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
-                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
-               :: "memory");
+// N consecutive columns of this warp's 32 TMEM lanes, here when it returns
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float* v) {
+  if constexpr (N == 32) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+          "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+          "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]),
+          "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]),
+          "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+                 : "r"(taddr));
+  } else if constexpr (N == 16) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+          "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+          "=f"(v[14]), "=f"(v[15])
+                 : "r"(taddr));
+  } else {
+    static_assert(N == 8, "8, 16 or 32 columns");
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+          "=f"(v[7])
+                 : "r"(taddr));
+  }
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));  // not used before the wait
 }
 
 }  // namespace
 
-// Warps 0-7 promote and store (TMEM lanes 32 (w % 4).., column half w / 4), warp
-// 8 issues the TMA loads, warp 9 the MMAs.  Every role walks the tiles
-// blockIdx.x, + gridDim.x, ... (token tile fastest).
+// The order of the tiles: bands of kF8Band token tiles, inside a band the token
+// tile fastest, so that the CTAs at work at one time share both their tokens
+// and their weights.  8192 x 8192 x 4096: 400 us with bands of 8 (4, 16, 32:
+// 413, 418, 415), 450 us with all token tiles in one.
+constexpr int kF8Band = 8;
+__device__ __forceinline__ void tile_place(const F8Params& p, int tile, int& m, int& n) {
+  const int per = kF8Band * p.tiles_n, band = tile / per, in = tile - band * per;
+  const int rows = min(kF8Band, p.tiles_m - band * kF8Band);
+  m = band * kF8Band + in % rows;
+  n = in / rows;
+}
+
+// Warps 0-15 promote and store (TMEM lanes 32 (w % 4).., column quarter w / 4),
+// warp 16 issues the TMA loads, warp 17 the MMAs.  Every role walks the tiles
+// blockIdx.x, + gridDim.x, ...
 template <int BN>
 __global__ void __launch_bounds__(kF8Threads, 1)
 f8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const F8Params p) {
@@ -255,43 +407,46 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
   pdl_wait();  // the tokens' codes and scales
 
   if (warp < kF8EpiWarps) {
-    constexpr int HALF = BN / 2, NC = HALF / 16;
-    const int q = warp & 3, half = warp >> 2;
-    const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(half * HALF);
+    // a warp's columns, and those it reads at once (a thread of 18 warps has 96 registers)
+    constexpr int COLS = BN / 4, CH = COLS == 64 ? 16 : COLS;
+    const int q = warp & 3, part = warp >> 2;
+    const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(part * COLS);
     int it = 0;  // K blocks so far: buffer it % 2
     bool ok = true;
     for (int tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x) {
-      const int m0 = (tile % p.tiles_m) * kF8TileM, n0 = (tile / p.tiles_m) * BN + half * HALF;
+      int tm, tn;
+      tile_place(p, tile, tm, tn);
+      const int m0 = tm * kF8TileM, n0 = tn * BN + part * COLS;
       const int row = m0 + 32 * q + lane;
       const float* sx = p.sx + row;  // rows up to tpad exist
       const float* sw = p.sw + (size_t)min(n0 / kF8Block, (p.N - 1) / kF8Block) * p.kb;
-      float acc[HALF];
+      float acc[COLS];
 #pragma unroll
-      for (int j = 0; j < HALF; ++j) acc[j] = 0.f;
-      float s_next = __ldcg(sx) * __ldg(sw);
+      for (int j = 0; j < COLS; ++j) acc[j] = 0.f;
+      float sx_next = __ldcg(sx), sw_next = __ldg(sw);  // a block ahead, multiplied when it is their turn
 #pragma unroll 1
       for (int kb = 0; kb < p.kb; ++kb, ++it) {
         const int b = it & 1;
-        const float s = s_next;
-        if (kb + 1 < p.kb) s_next = __ldcg(sx + (size_t)(kb + 1) * p.tpad) * __ldg(sw + kb + 1);
+        const float s = sx_next * sw_next;
+        if (kb + 1 < p.kb) {
+          sx_next = __ldcg(sx + (size_t)(kb + 1) * p.tpad);
+          sw_next = __ldg(sw + kb + 1);
+        }
         if (lane == 0) ok = tc_wait(&accf[b], (it >> 1) & 1, p.err, abort_flag, p.wait_ns);
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
         tc_fence_after();
-        float v[2][16];
-        tmem_ld16_async(tb + b * BN, v[0]);
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          tmem_wait16(v[c & 1]);
-          if (c + 1 < NC) {
-            tmem_ld16_async(tb + b * BN + 16 * (c + 1), v[(c + 1) & 1]);
-          } else {  // everything is read: the buffer may be overwritten
+        for (int c = 0; c < COLS; c += CH) {
+          float v[CH];
+          tmem_ld<CH>(tb + b * BN + c, v);
+          if (c + CH == COLS) {  // everything is read: the buffer may be overwritten
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&acce[b]);
           }
 #pragma unroll
-          for (int j = 0; j < 16; ++j) acc[16 * c + j] = fmaf(v[c & 1][j], s, acc[16 * c + j]);
+          for (int j = 0; j < CH; ++j) acc[c + j] = fmaf(v[j], s, acc[c + j]);
         }
       }
       if (!ok) break;
@@ -300,7 +455,7 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
         if (p.out_bf16) {
           __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + at;
 #pragma unroll
-          for (int j = 0; j < HALF; j += 8) {
+          for (int j = 0; j < COLS; j += 8) {
             if (p.vec && n0 + j + 8 <= p.N) {
               __nv_bfloat162 r[4];
 #pragma unroll
@@ -315,7 +470,7 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
         } else {
           float* o = static_cast<float*>(p.out) + at;
 #pragma unroll
-          for (int j = 0; j < HALF; j += 4) {
+          for (int j = 0; j < COLS; j += 4) {
             if (p.vec && n0 + j + 4 <= p.N) {
               *reinterpret_cast<float4*>(o + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
             } else {
@@ -332,7 +487,9 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
       int g = 0;
       bool ok = (int)blockIdx.x != p.skip_cta;
       for (int tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x) {
-        const int m0 = (tile % p.tiles_m) * kF8TileM, n0 = (tile / p.tiles_m) * BN;
+        int tm, tn;
+        tile_place(p, tile, tm, tn);
+        const int m0 = tm * kF8TileM, n0 = tn * BN;
 #pragma unroll 1
         for (int kb = 0; kb < p.kb; ++kb, ++g) {
           const int s = g % S;
@@ -396,6 +553,8 @@ cudaError_t setup_fp8_linear() {
   if (e == cudaSuccess) e = setup_tile<64>();
   if (e == cudaSuccess) e = setup_tile<128>();
   if (e == cudaSuccess) e = setup_tile<256>();
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(f8_gemv_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kF8GemvSmem);
   return e;
 }
 
@@ -429,8 +588,25 @@ static cudaError_t launch_dependent(void (*kernel)(A...), int grid, int threads,
   return cudaLaunchKernelEx(&c, kernel, args...);
 }
 
-cudaError_t launch_f8_gemv(const F8Params& p, cudaStream_t s) {
-  return launch_dependent(f8_gemv_kernel, (p.N + kGemvRows - 1) / kGemvRows, kGemvWarps * 32, 0, s, p);
+cudaError_t launch_f8_gemv(const F8Params& p, int sms, bool fused, cudaStream_t s) {
+  const int groups = (p.N + kGemvRows - 1) / kGemvRows;
+  int grid = groups < 2 * sms ? groups : 2 * sms;
+  if (!fused) return launch_dependent(f8_gemv_kernel<false>, grid, kGemvWarps * 32, 0, s, p);
+  // a CTA alone quantises 64 blocks of 128 inputs in one round of loads
+  const int cluster = p.T * p.kb > 64 && grid >= 4 ? 4 : 1;
+  grid = (grid + cluster - 1) / cluster * cluster;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3((unsigned)grid);
+  c.blockDim = dim3(kGemvWarps * 32);
+  c.dynamicSmemBytes = f8_gemv_smem(p.T, p.kb);
+  c.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)cluster;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  c.attrs = at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, f8_gemv_kernel<true>, p);
 }
 
 cudaError_t launch_f8_gemm(const F8Maps& m, const F8Params& p, int tile, int ctas, cudaStream_t s) {

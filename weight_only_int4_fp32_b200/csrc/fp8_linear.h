@@ -16,6 +16,10 @@ constexpr int kF8TileM = 128;     // tokens per tensor-core tile
 constexpr int kF8TileNs = 4;      // output tile widths 32, 64, 128, 256
 __host__ __device__ constexpr int f8_tile_n(int i) { return 32 << i; }
 
+// shared memory of the streaming kernel with T tokens' codes and scales, and its limit (two CTAs per SM)
+constexpr int kF8GemvSmem = 104 * 1024;
+__host__ __device__ constexpr size_t f8_gemv_smem(int T, int kb) { return (size_t)T * ((size_t)kb * kF8Block + 64 + 4 * kb); }
+
 struct F8Maps {
   CUtensorMap x;                  // token codes, boxes of 128 rows
   CUtensorMap w[kF8TileNs];       // weight codes, boxes of f8_tile_n(i) rows
@@ -24,6 +28,9 @@ struct F8Maps {
 struct F8Params {
   const uint8_t* w;   // codes [rows padded to 128][kb * 128]
   const float* sw;    // [ceil(N / 128)][kb]
+  const __nv_bfloat16* x;  // tokens (the streaming kernel quantises them itself)
+  long long x_stride;
+  int K, x_vec;
   const uint8_t* xq;  // codes [rows padded to 128][kb * 128]
   const float* sx;    // [kb][tpad]
   void* out;
@@ -40,7 +47,8 @@ cudaError_t f8_encode_maps(F8Maps* m, const uint8_t* w, int w_rows, const uint8_
 // x (bf16, row stride in elements) -> codes and scales
 cudaError_t launch_f8_quantize(const __nv_bfloat16* x, long long x_stride, int T, int K, int kb, int tpad,
                                uint8_t* xq, float* sx, cudaStream_t s);
-cudaError_t launch_f8_gemv(const F8Params& p, cudaStream_t s);
+// fused: quantises p.x itself (f8_gemv_smem within kF8GemvSmem); otherwise p.xq and p.sx are filled
+cudaError_t launch_f8_gemv(const F8Params& p, int sms, bool fused, cudaStream_t s);
 cudaError_t launch_f8_gemm(const F8Maps& m, const F8Params& p, int tile, int ctas, cudaStream_t s);
 
 }  // namespace lingmoe
