@@ -76,24 +76,30 @@ def step_bound(q, k, v, g, beta, state, scale):
 
 
 def prefill_bound(q, k, v, g, beta, state, scale):
-    """The same for the chunked prefill of one sequence: (out's error [T, Hv, dv], the last state's by column [Hv, dv],
-    the last state's by element [Hv, dk, dv]: what the last chunk's own arithmetic adds).
+    """The same for the chunked prefill of one sequence: (out's error [T, Hv, dv], the last state's by column [Hv, dv]).
 
-    Chunks of 64 tokens:  X = V - Kt S0,  U = T diag(b) X,  O = Qt S0 + B U,
-    S1 = D S0 + Kh^T U with T = (I + A)^-1.  Every decay is a product of at most
+    Chunks of 64 tokens:  (I + A) [W, U~] = diag(b) [Kt, V],  U = U~ - W S0,
+    O = Qt S0 + B U,  S1 = D S0 + Kh^T U.  Every decay is a product of at most
     64 exps (5 u each with its product), a key's norm 9 u, the joins a few more:
     eta = 360 u.  Operands that feed the state are two fp16 terms (2^-22 of the
-    value, at least 2^-35 at their scale of 2^10; block-scaled ones at least
-    2^-37 of the block's largest), with the product of the two low terms left
-    out and 16 u of fp32 sums: mm = 3 2^-22 + 16 u of the magnitudes.  The fp16
-    operands of the output: 2^-11 each.  The inverse: 128 u |T| (|I + A|) |T|."""
+    value, at least 2^-35 at the fixed scale of 2^10; scaled by their largest at
+    least 2^-37 of it), with the product of the two low terms left out and 16 u
+    of fp32 sums: mm = 3 2^-22 + 16 u of the magnitudes.  The fp16 operands of
+    the output: 2^-11 each.
+
+    The solution Z of (I + A) Z = R by 16-row blocks: what is computed solves the
+    system up to the residual of  A's error E and its products (E + mm |A|) |Z|,
+    R's error, 8 u of the sums, and the diagonal blocks' inverses Td, formed by
+    16 steps of substitution (32 u |Td| |Ld| |Td|), split and multiplied:
+    |Ld| (32 u |Td| |Ld| |Td| + (2^-22 + mm) |Td|) |Ld| |Z|.  Its error is |(I + A)^-1|
+    times that, and 2^-22 |Z| for the terms that are kept."""
     q, k, v, a, b = heads(q, k, v, g, beta)
     T_, H = b.shape
     S = np.asarray(state, np.float64).copy()
     e = np.zeros((H, S.shape[2]))
     out = np.empty(v.shape)
     eta, mm, h16, tiny = 360 * U, 3 * 2.0**-22 + 16 * U, 2.0**-11, 2.0**-35
-    last = np.zeros(S.shape)
+    ab = np.abs
     with np.errstate(divide="ignore"):
         la = np.log(a)
     for c in range(0, T_, CHUNK):
@@ -109,26 +115,36 @@ def prefill_bound(q, k, v, g, beta, state, scale):
                 dec[:, i, j] = dec[:, i - 1, j] * np.exp(lc[:, i])
         first = dec[:, :, 0] * np.exp(lc[:, :1])     # [h, i, c] = prod a over the chunk's first i + 1
         to_end = dec[:, n - 1]                       # [h, j, c]
-        low, strict = np.tril(np.ones((n, n))), np.tril(np.ones((n, n)), -1)
+        low, strict, eye = np.tril(np.ones((n, n))), np.tril(np.ones((n, n)), -1), np.eye(n)
         A = np.einsum("hic,hijc,hjc->hij", kc, dec, kc) * strict * bc[:, :, None]
-        Am = np.einsum("hic,hijc,hjc->hij", np.abs(kc), dec, np.abs(kc)) * strict * np.abs(bc)[:, :, None]
+        Am = np.einsum("hic,hijc,hjc->hij", ab(kc), dec, ab(kc)) * strict * ab(bc)[:, :, None]
         B = np.einsum("hic,hijc,hjc->hij", qc, dec, kc) * low
-        Bm = np.einsum("hic,hijc,hjc->hij", np.abs(qc), dec, np.abs(kc)) * low
+        Bm = np.einsum("hic,hijc,hjc->hij", ab(qc), dec, ab(kc)) * low
         del dec
-        Ti = np.linalg.inv(np.eye(n) + A) * low
-        TB, Ta = Ti * bc[:, None, :], np.abs(Ti)
+        Ti = np.linalg.inv(eye + A) * low
+        Ta = ab(Ti)
+        blocks = (np.arange(n)[:, None] // 16 == np.arange(n)[None, :] // 16) * low
+        Ld, Td = ab(eye + A) * blocks, Ta * blocks  # a triangular inverse's diagonal blocks are its blocks' inverses
         Kt, Qt, Kh, D = kc * first, qc * first, kc * to_end, first[:, n - 1]
-        X = vc - Kt @ S
-        Uc = TB @ X
+        E = (eta + mm) * Am + tiny * strict
+        inv = Ld @ (32 * U * Td @ Ld @ Td + (2.0**-22 + mm) * Td + tiny * blocks) @ Ld
+
+        def solve(R, r_err):
+            Z = Ti @ (bc[:, :, None] * R)
+            za = ab(Z) + 2.0**-36 * (ab(eye + A) @ ab(Z)).max(axis=1, keepdims=True)
+            resid = r_err * ab(bc)[:, :, None] * ab(R) + (E + mm * ab(A)) @ za + inv @ za \
+                + 8 * U * (ab(bc)[:, :, None] * ab(R) + ab(A) @ ab(Z))
+            return Z, Ta @ resid + 2.0**-22 * ab(Z)
+
+        W, dW = solve(Kt, eta)
+        Ut, dUt = solve(vc, 2 * U)
+        dW = dW + tiny
+        Uc = Ut - W @ S
         O = Qt @ S + B @ Uc
         S1 = D[:, :, None] * S + np.swapaxes(Kh, 1, 2) @ Uc
-        ab = np.abs
-        top = lambda x: ab(x).max(axis=(1, 2), keepdims=True) * 2.0**-37  # noqa: E731
-        Sa, Xa, Ua = ab(S) + top(S), ab(X) + top(X), ab(Uc) + top(Uc)
-        dX = ((eta + mm) * ab(Kt) + tiny) @ Sa + 8 * U * ab(X) + 10 * U * (ab(vc) + ab(Kt) @ Sa)
-        dT = Ta @ ((eta + mm) * Am + tiny) @ Ta + 128 * U * Ta @ (ab(A) + np.eye(n)) @ Ta + 2.0**-22 * Ta
-        dTB = (dT + 2 * U * Ta) * ab(bc)[:, None, :] + tiny * low
-        dU = ab(TB) @ dX + dTB @ Xa + mm * ab(TB) @ Xa
+        top = lambda x: ab(x).max(axis=1, keepdims=True) * 2.0**-37  # noqa: E731  by column
+        Sa, Ua = ab(S) + top(S), ab(Uc) + top(Uc)
+        dU = (dW + mm * ab(W)) @ Sa + dUt + 8 * U * (ab(Ut) + ab(W) @ ab(S))
         dS = 330 * U * D[:, :, None] * ab(S) + np.swapaxes(ab(Kh), 1, 2) @ dU \
             + np.swapaxes((eta + mm) * ab(Kh) + tiny, 1, 2) @ Ua + 10 * U * (ab(S1) + D[:, :, None] * ab(S))
         dUe = dU + ab(bc)[:, :, None] * e[:, None, :]
@@ -137,6 +153,5 @@ def prefill_bound(q, k, v, g, beta, state, scale):
         out[sl] = np.swapaxes(abs(scale) * dO, 0, 1)
         shrink = np.prod(np.swapaxes(np.exp(lc), 1, 2).max(1), axis=1)  # [H]: product over tokens of max(a)
         e = shrink[:, None] * e + np.linalg.norm(dS, axis=1) + 1e-37
-        last = dS
         S = S1
-    return out, e, last
+    return out, e

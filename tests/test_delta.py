@@ -54,8 +54,8 @@ def test_bounds_are_positive_and_cover_fp32(T):
         S = S + kn[t][:, :, None] * u[:, None]
         assert (np.linalg.norm(S - states[t], axis=1) <= e[t]).all()
         assert (np.abs(0.125 * np.einsum("hkv,hk->hv", S, qn[t]) - out[t]) <= o[t]).all()
-    po, pe, last = D.prefill_bound(q, k, v, g, b, s0, 0.125)
-    assert np.isfinite(po).all() and (po > 0).all() and (pe > 0).all() and (last > 0).all()
+    po, pe = D.prefill_bound(q, k, v, g, b, s0, 0.125)
+    assert np.isfinite(po).all() and (po > 0).all() and (pe > 0).all()
     assert pe.max() < 0.01 * np.linalg.norm(states[-1], axis=1).max()
 
 

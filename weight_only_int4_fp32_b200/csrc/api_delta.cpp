@@ -13,9 +13,9 @@ namespace {
 
 constexpr unsigned long long kWaitNs = 2000000000ull;  // 2 s
 // Records (chunk x head) of the prefill's workspace: the operands of one
-// segment of chunks, about the size of half the L2, so that the scan reads
-// what the preparation has just written from there.
-constexpr int kRecords = 640;
+// segment of chunks, two waves of the preparation's CTAs (two per SM), about the
+// size of half the L2, so that the scan reads what has just been written from there.
+constexpr int kRecordsPerSm = 4;
 
 struct Span { const char* lo; const char* hi; };
 Span span(const void* p, size_t es, const int64_t n[4], const int64_t st[4]) {
@@ -130,9 +130,9 @@ int ling_moe_delta_create(const ling_moe_delta_config_t* cfg, ling_moe_delta_t**
   h->cfg = *cfg;
   if (h->cfg.scale == 0.f) h->cfg.scale = 1.f / std::sqrt((float)cfg->head_k);
   const int64_t need = chunks_bound(cfg->max_tokens, cfg->max_seqs);
-  const int64_t fit = kRecords / cfg->v_heads > 0 ? kRecords / cfg->v_heads : 1;
+  const int64_t fit = kRecordsPerSm * sms / cfg->v_heads > 0 ? kRecordsPerSm * sms / cfg->v_heads : 1;
   h->seg_chunks = (int)(need < fit ? need : fit);
-  e = cudaMalloc(&h->ws, (size_t)h->seg_chunks * cfg->v_heads * delta_rec_bytes(cfg->head_k));
+  e = cudaMalloc(&h->ws, (size_t)h->seg_chunks * cfg->v_heads * delta_rec_bytes(cfg->head_k, cfg->head_v));
   if (e == cudaSuccess) e = cudaMalloc(&h->err, sizeof(unsigned int));
   if (e == cudaSuccess) e = cudaMemset(h->err, 0, sizeof(unsigned int));
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
@@ -190,7 +190,7 @@ int ling_moe_delta_prefill(ling_moe_delta_t* h, const ling_moe_delta_io_t* io, i
     p.seg0 = (int)c;
     p.seg_chunks = (int)(all - c < h->seg_chunks ? all - c : h->seg_chunks);
     cudaError_t e = launch_delta_prep(p, h->cfg.head_k, s);
-    if (e == cudaSuccess) e = launch_delta_scan(p, h->cfg.head_k, s);
+    if (e == cudaSuccess) e = launch_delta_scan(p, h->cfg.head_k, h->sms, s);
     if (e != cudaSuccess) return fail_cuda(e, "delta rule prefill launch");
     h->launches.fetch_add(2);
   }

@@ -10,9 +10,10 @@
 // stands with the state in registers.  HBM bound: the state read and written once.
 //
 // Prefill: chunks of 64 tokens.  With G the running sum of g inside a chunk,
-//   A[i,j] = b_i sum_c k_i k_j exp(G_i - G_j)  (j < i),   T = (I + A)^-1,
+//   A[i,j] = b_i sum_c k_i k_j exp(G_i - G_j)  (j < i),
 //   B[i,j] = sum_c q_i k_j exp(G_i - G_j)      (j <= i),
-//   X = v - (k exp G) S0,   U = (T diag(b)) X,
+//   (I + A) [W, U~] = diag(b) [k exp G, v],
+//   U = U~ - W S0,
 //   O = (q exp G) S0 + B U,   S1 = diag(exp G_last) S0 + (k exp(G_last - G))^T U.
 // delta_prep_kernel forms, for every chunk and head at once, the operands
 // that do not depend on the state; delta_scan_kernel walks a sequence's
@@ -22,9 +23,9 @@
 //
 // Precision: products run on mma.sync with fp16 operands and fp32 sums.  What
 // feeds the state (fp32) is split into two fp16 terms (22 bits) after a power-
-// of-two scale taken from each 16-row block's largest value, three products
-// per pair of split operands; what feeds only the bf16 output takes one fp16
-// term (half a step 2^-11, the output's own being 2^-8).
+// of-two scale taken from each row's largest value (fixed where the values are
+// bounded), three products per pair of split operands; what feeds only the bf16
+// output takes one fp16 term (half a step 2^-11, the output's own being 2^-8).
 #include "common.cuh"
 #include "delta.h"
 
@@ -36,6 +37,9 @@ constexpr float kOpScale = 1024.f;  // k, q, T and B operands are stored times 2
 constexpr float kNormEps = 1e-6f;
 constexpr unsigned long long kLandNs = 2000000000ull;
 
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared.b64 _, [%0];" :: "r"(smem_u32(bar)) : "memory");
+}
 __device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t r[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
@@ -422,41 +426,65 @@ __global__ void __launch_bounds__(256, 2) delta_step_kernel(const DeltaParams p)
 // through the border between them.  Only the 8 x 8 blocks on the diagonal are
 // left; their pairs are summed directly from running products.
 //
-// The record of a chunk and head (layout: rows of 2 dk or 128 bytes, 16-byte
-// pieces exchanged by piece ^= row % 8 for conflict-free ldmatrix):
-//   k exp(G) hi, lo | q exp(G) | T diag(b) hi, lo | B | exp(G_last) fp32 |
-//   k exp(G_last - G) hi, lo
+// (I + A) [W U~] = diag(b) [k exp(G), v] is then solved by 16-row blocks, the
+// right sides transposed: a warp takes 16 of the 2 x 128 columns through all four
+// blocks in registers (what a product leaves is the next one's operand), with the
+// inverses of the diagonal blocks formed by substitution before.
+//
+// The record of a chunk and head: W^T hi, lo [dk][64] | q exp(G) [64][dk] |
+// k exp(G_last - G) hi, lo [64][dk] | B [64][64] | exp(G_last) fp32 [dk] | U~^T fp32
+// in the order of the accumulators that take it.  fp16 rows have their 16-byte
+// pieces exchanged, piece ^= row % 8, for conflict-free ldmatrix.
 template <int DK>
 struct PrepCfg {
-  static constexpr int kRow = DK * 2 + 16;      // bytes of a k or q row in shared memory
-  static constexpr int kPRow = DK + 8;          // floats of a p or s row
-  static constexpr int kMRow = 68;              // floats of a row of a 64 x 64 matrix
-  static constexpr int kK = 0, kQ = kDeltaChunk * kRow;
-  static constexpr int kP = 2 * kDeltaChunk * kRow;
-  static constexpr int kS = kP + kDeltaChunk * kPRow * 4;
-  static constexpr int kEnd = kS + kDeltaChunk * kPRow * 4;
-  // the matrices take the place of the operands once the products are done
+  static constexpr int kFRow = DK + 8;            // floats of a row of k p or k s
+  static constexpr int kHRow = DK * 2 + 16;       // bytes of a row of q p
+  static constexpr int kVRow = 128 * 2 + 16;      // bytes of a row of v
+  static constexpr int kMRow = 68;                // floats of a row of a 64 x 64 matrix
   static constexpr int kMat = kDeltaChunk * kMRow * 4;
-  static constexpr int kT = kEnd > 3 * kMat ? kEnd : 3 * kMat;  // t [8][DK]
-  static constexpr int kRk = kT + 8 * DK * 4, kRq = kRk + 256, kB = kRq + 256, kInfo = kB + 256;
-  static constexpr int kSmem = kInfo + 32;
+  static constexpr int max2(int a, int b) { return a > b ? a : b; }
+  static constexpr int oKp = 0;
+  static constexpr int oKs = oKp + kDeltaChunk * kFRow * 4;
+  static constexpr int oQ = oKs + max2(kDeltaChunk * kFRow * 4, 2 * kMat);
+  static constexpr int oQ8 = oQ + max2(kDeltaChunk * kHRow, kDeltaChunk * kVRow);  // second halves of the tiles
+  static constexpr int oT = oQ8 + kDeltaChunk / 2 * kHRow;                         // t [8][DK]
+  static constexpr int oBefore = oT + 8 * DK * 4;                                  // [8][DK]
+  static constexpr int oB = oBefore + 8 * DK * 4, oInfo = oB + 256;
+  static constexpr int kSmem = oInfo + 32;
+  // once the products are done: A and B in place of k s, v in place of q p, then
+  // A's blocks below the diagonal and the inverses on it as fp16 in place of B
+  static constexpr int oA = oKs, oBm = oKs + kMat, oV = oQ, oA16 = oBm;
+  static_assert(2 * kDeltaChunk * 128 <= kMat, "A as fp16 hi and lo");
 };
+
+// Four values of two rows (rows gq and gq + 8 of a 16 x 8 accumulator pair) as an
+// A operand of two fp16 terms, each row times its scale
+__device__ __forceinline__ void split_frag(const float x[4], const float y[4], float s0, float s1, uint32_t hi[4],
+                                           uint32_t lo[4]) {
+  split2(x[0] * s0, x[1] * s0, hi[0], lo[0]);
+  split2(x[2] * s1, x[3] * s1, hi[1], lo[1]);
+  split2(y[0] * s0, y[1] * s0, hi[2], lo[2]);
+  split2(y[2] * s1, y[3] * s1, hi[3], lo[3]);
+}
+// the largest of a row, held by the four lanes of a quad
+__device__ __forceinline__ float quad_max(float m) {
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  return fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+}
 
 template <int DK>
 __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p) {
   using C = PrepCfg<DK>;
   constexpr int CPL = DK / 32;
   extern __shared__ __align__(128) unsigned char dsm[];
-  float* sp = reinterpret_cast<float*>(dsm + C::kP);
-  float* ss = reinterpret_cast<float*>(dsm + C::kS);
-  float* st = reinterpret_cast<float*>(dsm + C::kT);
-  float* srk = reinterpret_cast<float*>(dsm + C::kRk);
-  float* srq = reinterpret_cast<float*>(dsm + C::kRq);
-  float* sbeta = reinterpret_cast<float*>(dsm + C::kB);
-  int* info = reinterpret_cast<int*>(dsm + C::kInfo);
-  float* mA = reinterpret_cast<float*>(dsm);
-  float* mB = reinterpret_cast<float*>(dsm + C::kMat);
-  float* mT = reinterpret_cast<float*>(dsm + 2 * C::kMat);
+  float* skp = reinterpret_cast<float*>(dsm + C::oKp);
+  float* sks = reinterpret_cast<float*>(dsm + C::oKs);
+  float* st = reinterpret_cast<float*>(dsm + C::oT);
+  float* sbefore = reinterpret_cast<float*>(dsm + C::oBefore);
+  float* sbeta = reinterpret_cast<float*>(dsm + C::oB);
+  int* info = reinterpret_cast<int*>(dsm + C::oInfo);
+  float* mA = reinterpret_cast<float*>(dsm + C::oA);
+  float* mB = reinterpret_cast<float*>(dsm + C::oBm);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int h = blockIdx.y, hk = h / (p.Hv / p.Hk);
   if (warp == 0) {
@@ -470,7 +498,7 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
   __syncthreads();
   const int len = info[0], start = info[1];
   if (len == 0) return;
-  unsigned char* rec = p.ws + ((size_t)blockIdx.x * p.Hv + h) * delta_rec_bytes(DK);
+  unsigned char* rec = p.ws + ((size_t)blockIdx.x * p.Hv + h) * delta_rec_bytes(DK, p.dv);
 
   // ---- this warp's 8 rows, CPL channels per lane
   const int row0 = 8 * warp, c0 = CPL * lane;
@@ -492,60 +520,74 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
     const int r = row0 + lane;
     sbeta[r] = r < len ? p.beta[(long long)(start + r) * p.be_t + h * p.be_h] : 0.f;
   }
+  {
+    float n[16];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float qq = 0.f, kk = 0.f;
+    for (int i = 0; i < 8; ++i) {
+      n[i] = n[8 + i] = 0.f;
 #pragma unroll
-    for (int c = 0; c < CPL; ++c) qq += q[i][c] * q[i][c], kk += k[i][c] * k[i][c];
-    const float rq = 1.f / sqrtf(warp_sum(qq) + kNormEps), rk = 1.f / sqrtf(warp_sum(kk) + kNormEps);
-    uint32_t kw[CPL / 2], qw[CPL / 2];
-#pragma unroll
-    for (int c = 0; c < CPL / 2; ++c) {  // back to the bf16 they came from: exact
-      const __nv_bfloat162 kb = __floats2bfloat162_rn(k[i][2 * c], k[i][2 * c + 1]);
-      const __nv_bfloat162 qb = __floats2bfloat162_rn(q[i][2 * c], q[i][2 * c + 1]);
-      kw[c] = *reinterpret_cast<const uint32_t*>(&kb);
-      qw[c] = *reinterpret_cast<const uint32_t*>(&qb);
+      for (int c = 0; c < CPL; ++c) n[i] = fmaf(q[i][c], q[i][c], n[i]), n[8 + i] = fmaf(k[i][c], k[i][c], n[8 + i]);
     }
+    // lanes 2 i and 2 i + 1 are left with the sum of n[i]
 #pragma unroll
-    for (int c = 0; c < CPL / 2; ++c) {
-      *reinterpret_cast<uint32_t*>(dsm + C::kK + (row0 + i) * C::kRow + 2 * c0 + 4 * c) = kw[c];
-      *reinterpret_cast<uint32_t*>(dsm + C::kQ + (row0 + i) * C::kRow + 2 * c0 + 4 * c) = qw[c];
-    }
-    if (lane == 0) {
-      srk[row0 + i] = rk;
-      srq[row0 + i] = rq;
-    }
+    for (int o = 8; o > 0; o >>= 1) {
+      const bool up = lane & (2 * o);
 #pragma unroll
-    for (int c = 0; c < CPL; ++c) {
-      k[i][c] *= rk;
-      q[i][c] *= rq;
-      a[i][c] = decay_of(a[i][c]);
+      for (int i = 0; i < o; ++i) {
+        const float keep = up ? n[i + o] : n[i], send = up ? n[i] : n[i + o];
+        n[i] = keep + __shfl_xor_sync(0xffffffffu, send, 2 * o);
+      }
+    }
+    const float r = 1.f / sqrtf(n[0] + __shfl_xor_sync(0xffffffffu, n[0], 1) + kNormEps);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float rq = __shfl_sync(0xffffffffu, r, 2 * i), rk = __shfl_sync(0xffffffffu, r, 16 + 2 * i);
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) {
+        q[i][c] *= rq;
+        k[i][c] *= rk;
+        a[i][c] = decay_of(a[i][c]);
+      }
     }
   }
-  // prefix and suffix products of the block
+  auto store_row = [&](float* dst, const float* x) {
+    if constexpr (CPL == 4)
+      *reinterpret_cast<float4*>(dst) = make_float4(x[0], x[1], x[2], x[3]);
+    else
+      *reinterpret_cast<float2*>(dst) = make_float2(x[0], x[1]);
+  };
+  auto store_half = [&](unsigned char* dst, const float* x) {  // times the operands' scale
+    if constexpr (CPL == 4)
+      *reinterpret_cast<uint2*>(dst) =
+          make_uint2(pack_half2(x[0] * kOpScale, x[1] * kOpScale), pack_half2(x[2] * kOpScale, x[3] * kOpScale));
+    else
+      *reinterpret_cast<uint32_t*>(dst) = pack_half2(x[0] * kOpScale, x[1] * kOpScale);
+  };
+  // k p and k s; the block's whole product; q p of a tile's second half (for its border)
   {
-    float x[CPL];
+    float x[CPL], y[CPL];
 #pragma unroll
     for (int c = 0; c < CPL; ++c) x[c] = 1.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 8; ++i) {
 #pragma unroll
-      for (int c = 0; c < CPL; ++c) {
-        x[c] *= a[i][c];
-        sp[(row0 + i) * C::kPRow + c0 + c] = x[c];
+      for (int c = 0; c < CPL; ++c) x[c] *= a[i][c], y[c] = k[i][c] * x[c];
+      store_row(skp + (row0 + i) * C::kFRow + c0, y);
+      if (warp & 1) {
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) y[c] = q[i][c] * x[c];
+        store_half(dsm + C::oQ8 + (8 * (warp >> 1) + i) * C::kHRow + 2 * c0, y);
       }
-#pragma unroll
-    for (int c = 0; c < CPL; ++c) {
-      st[warp * DK + c0 + c] = x[c];
-      x[c] = 1.f;
     }
+    store_row(st + warp * DK + c0, x);
 #pragma unroll
-    for (int i = 7; i >= 0; --i)
+    for (int c = 0; c < CPL; ++c) x[c] = 1.f;
 #pragma unroll
-      for (int c = 0; c < CPL; ++c) {
-        ss[(row0 + i) * C::kPRow + c0 + c] = x[c];
-        x[c] *= a[i][c];
-      }
+    for (int i = 7; i >= 0; --i) {
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) y[c] = k[i][c] * x[c], x[c] *= a[i][c];
+      store_row(sks + (row0 + i) * C::kFRow + c0, y);
+    }
   }
   // the pairs inside the block: entry i (i - 1) / 2 + j of each list for j < i,
   // then the q.k of equal rows (0-3 in the first list, 4-7 in the second)
@@ -554,27 +596,29 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
     float vk[32], vq[32];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      float x[CPL], y = 0.f;
+      f2 x[CPL / 2], y = 0ull;
 #pragma unroll
-      for (int c = 0; c < CPL; ++c) {
-        x[c] = k[j][c];
-        y += q[j][c] * x[c];
+      for (int c = 0; c < CPL / 2; ++c) {
+        x[c] = pack2(k[j][2 * c], k[j][2 * c + 1]);
+        y = fma2(pack2(q[j][2 * c], q[j][2 * c + 1]), x[c], y);
       }
+      const float2 yy = unpack2(y);
       if (j < 4)
-        vk[28 + j] = y;
+        vk[28 + j] = yy.x + yy.y;
       else
-        vq[24 + j] = y;
+        vq[24 + j] = yy.x + yy.y;
 #pragma unroll
       for (int i = j + 1; i < 8; ++i) {
-        float u = 0.f, w = 0.f;
+        f2 u = 0ull, w = 0ull;
 #pragma unroll
-        for (int c = 0; c < CPL; ++c) {
-          x[c] *= a[i][c];
-          u = fmaf(k[i][c], x[c], u);
-          w = fmaf(q[i][c], x[c], w);
+        for (int c = 0; c < CPL / 2; ++c) {
+          x[c] = mul2(x[c], pack2(a[i][2 * c], a[i][2 * c + 1]));
+          u = fma2(pack2(k[i][2 * c], k[i][2 * c + 1]), x[c], u);
+          w = fma2(pack2(q[i][2 * c], q[i][2 * c + 1]), x[c], w);
         }
-        vk[i * (i - 1) / 2 + j] = u;
-        vq[i * (i - 1) / 2 + j] = w;
+        const float2 uu = unpack2(u), ww = unpack2(w);
+        vk[i * (i - 1) / 2 + j] = uu.x + uu.y;
+        vq[i * (i - 1) / 2 + j] = ww.x + ww.y;
       }
     }
     dkk = transpose_sum32(vk);
@@ -582,11 +626,11 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
   }
   __syncthreads();
 
-  // ---- the operands that meet the state
+  // ---- the operands that meet the state, and q p of the tiles
   {
     float before[CPL], after[CPL];
 #pragma unroll
-    for (int c = 0; c < CPL; ++c) before[c] = after[c] = kOpScale;
+    for (int c = 0; c < CPL; ++c) before[c] = after[c] = 1.f;
     for (int w = 0; w < 8; ++w)
 #pragma unroll
       for (int c = 0; c < CPL; ++c) {
@@ -594,38 +638,48 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
         if (w < warp) before[c] *= t;
         if (w > warp) after[c] *= t;
       }
+    store_row(sbefore + warp * DK + c0, before);
+    float x[CPL], first[CPL];
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) {
+      x[c] = 1.f;
+      first[c] = warp & 1 ? st[(warp - 1) * DK + c0 + c] : 1.f;
+    }
     constexpr int KT = delta_tile_bytes(DK);
-    unsigned char* khat = rec + 3 * KT + delta_ta_bytes(DK);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int r = row0 + i;
       const size_t at = (size_t)r * DK * 2 + (((2 * c0) >> 4) ^ (r & 7)) * 16 + ((2 * c0) & 15);
-      float kt[CPL], qt[CPL], kh[CPL];
+      float qt[CPL], qp[CPL], kh[CPL];
 #pragma unroll
       for (int c = 0; c < CPL; ++c) {
-        const float e = before[c] * sp[r * C::kPRow + c0 + c];
-        kt[c] = k[i][c] * e;
-        qt[c] = q[i][c] * e;
-        kh[c] = k[i][c] * (after[c] * ss[r * C::kPRow + c0 + c]);
+        x[c] *= a[i][c];
+        const float y = q[i][c] * x[c];
+        qt[c] = y * before[c];
+        qp[c] = y * first[c];
+        kh[c] = after[c] * kOpScale * sks[r * C::kFRow + c0 + c];
       }
+      store_half(dsm + C::oQ + r * C::kHRow + 2 * c0, qp);
+      store_half(rec + 2 * KT + at, qt);
+      uint32_t hi[CPL / 2], lo[CPL / 2];
 #pragma unroll
-      for (int c = 0; c < CPL; c += 2) {
-        uint32_t hi, lo;
-        split2(kt[c], kt[c + 1], hi, lo);
-        *reinterpret_cast<uint32_t*>(rec + at + 2 * c) = hi;
-        *reinterpret_cast<uint32_t*>(rec + KT + at + 2 * c) = lo;
-        *reinterpret_cast<uint32_t*>(rec + 2 * KT + at + 2 * c) = pack_half2(qt[c], qt[c + 1]);
-        split2(kh[c], kh[c + 1], hi, lo);
-        *reinterpret_cast<uint32_t*>(khat + at + 2 * c) = hi;
-        *reinterpret_cast<uint32_t*>(khat + KT + at + 2 * c) = lo;
+      for (int c = 0; c < CPL / 2; ++c) split2(kh[2 * c], kh[2 * c + 1], hi[c], lo[c]);
+      if constexpr (CPL == 4) {
+        *reinterpret_cast<uint2*>(rec + 3 * KT + at) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(rec + 4 * KT + at) = make_uint2(lo[0], lo[1]);
+      } else {
+        *reinterpret_cast<uint32_t*>(rec + 3 * KT + at) = hi[0];
+        *reinterpret_cast<uint32_t*>(rec + 4 * KT + at) = lo[0];
       }
     }
     if (warp == 7) {  // nothing after the last block: exp(G_last) = before x its own product
-      float* dec = reinterpret_cast<float*>(rec + 3 * KT + 3 * kDeltaChunk * kDeltaChunk * 2);
+      float y[CPL];
 #pragma unroll
-      for (int c = 0; c < CPL; ++c) dec[c0 + c] = before[c] * (1.f / kOpScale) * st[7 * DK + c0 + c];
+      for (int c = 0; c < CPL; ++c) y[c] = before[c] * st[7 * DK + c0 + c];
+      store_row(reinterpret_cast<float*>(rec + 5 * KT + kDeltaChunk * kDeltaChunk * 2) + c0, y);
     }
   }
+  __syncthreads();
 
   // ---- tile row a of A and B, half the channels per warp
   const int ta = warp & 3, hh = warp >> 2, gq = lane >> 2, tq = lane & 3;
@@ -636,7 +690,6 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
     for (int e = 0; e < 4; ++e) accA[u][e] = accB[u][e] = 0.f;
   {
     const int r0 = 16 * ta + gq, r1 = r0 + 8;
-    const float rk0 = srk[r0] * kOpScale, rk1 = srk[r1] * kOpScale, rq0 = srq[r0] * kOpScale, rq1 = srq[r1] * kOpScale;
 #pragma unroll 1
     for (int ks = hh * (DK / 32); ks < (hh + 1) * (DK / 32); ++ks) {
       uint32_t Ah[4], Al[4], Aq[4], Rh[4], Rl[4], Rq[4];
@@ -644,77 +697,81 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
 #pragma unroll
       for (int half = 0; half < 2; ++half) {  // channels 2 tq, + 1 and + 8, + 9
         const int c = 16 * ks + 8 * half + 2 * tq;
-        const uint32_t k0 = *reinterpret_cast<const uint32_t*>(dsm + C::kK + r0 * C::kRow + 2 * c);
-        const uint32_t k1 = *reinterpret_cast<const uint32_t*>(dsm + C::kK + r1 * C::kRow + 2 * c);
-        const uint32_t q0 = *reinterpret_cast<const uint32_t*>(dsm + C::kQ + r0 * C::kRow + 2 * c);
-        const uint32_t q1 = *reinterpret_cast<const uint32_t*>(dsm + C::kQ + r1 * C::kRow + 2 * c);
-        const float2 p0 = *reinterpret_cast<const float2*>(sp + r0 * C::kPRow + c);
-        const float2 p1 = *reinterpret_cast<const float2*>(sp + r1 * C::kPRow + c);
+        const float2 k0 = *reinterpret_cast<const float2*>(skp + r0 * C::kFRow + c);
+        const float2 k1 = *reinterpret_cast<const float2*>(skp + r1 * C::kFRow + c);
         const float2 t0 = *reinterpret_cast<const float2*>(st + 2 * ta * DK + c);
-        D[half][0] = D[half][1] = 1.f;
-        split2(bf16lo(k0) * rk0 * p0.x, bf16hi(k0) * rk0 * p0.y, Ah[2 * half], Al[2 * half]);
-        Aq[2 * half] = pack_half2(bf16lo(q0) * rq0 * p0.x, bf16hi(q0) * rq0 * p0.y);
-        const float kx = bf16lo(k1) * rk1 * p1.x, ky = bf16hi(k1) * rk1 * p1.y;
-        const float qx = bf16lo(q1) * rq1 * p1.x, qy = bf16hi(q1) * rq1 * p1.y;
+        D[half][0] = D[half][1] = kOpScale;
+        const float kx = k1.x * kOpScale, ky = k1.y * kOpScale;
+        split2(k0.x * kOpScale, k0.y * kOpScale, Ah[2 * half], Al[2 * half]);
         split2(kx * t0.x, ky * t0.y, Ah[2 * half + 1], Al[2 * half + 1]);
-        Aq[2 * half + 1] = pack_half2(qx * t0.x, qy * t0.y);
         split2(kx, ky, Rh[2 * half + 1], Rl[2 * half + 1]);
-        Rq[2 * half + 1] = pack_half2(qx, qy);
+        Aq[2 * half] = *reinterpret_cast<const uint32_t*>(dsm + C::oQ + r0 * C::kHRow + 2 * c);
+        Aq[2 * half + 1] = *reinterpret_cast<const uint32_t*>(dsm + C::oQ + r1 * C::kHRow + 2 * c);
+        Rq[2 * half + 1] = *reinterpret_cast<const uint32_t*>(dsm + C::oQ8 + (8 * ta + gq) * C::kHRow + 2 * c);
         Rh[2 * half] = Rl[2 * half] = Rq[2 * half] = 0u;
       }
-      // column tile s of 8 rows: u = 6 the tile row's own first half, else s = 2 ta - 1 - u
+      // column tile s of 8 rows: unit 6 the tile row's own first half, else s = 2 ta - 1 - unit
 #pragma unroll
-      for (int u = 6; u >= -1; --u) {
-        if (u == -1) break;
-        const int uu = u == 6 ? 6 : 5 - u;  // 6, then 0, 1, .. 5
-        const int s = u == 6 ? 2 * ta : 2 * ta - 1 - uu;
+      for (int n = 0; n < 7; ++n) {
+        const int u = n == 0 ? 6 : n - 1;
+        const int s = u == 6 ? 2 * ta : 2 * ta - 1 - u;
         if (s >= 0) {
-          const int j = 8 * s + gq;
-          const float rk = srk[j] * kOpScale;
           uint32_t Bh[2], Bl[2];
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             const int c = 16 * ks + 8 * half + 2 * tq;
-            const uint32_t kj = *reinterpret_cast<const uint32_t*>(dsm + C::kK + j * C::kRow + 2 * c);
-            const float2 sj = *reinterpret_cast<const float2*>(ss + j * C::kPRow + c);
-            float x = bf16lo(kj) * rk * sj.x, y = bf16hi(kj) * rk * sj.y;
+            float2 kj = *reinterpret_cast<const float2*>(sks + (8 * s + gq) * C::kFRow + c);
+            kj.x *= D[half][0];
+            kj.y *= D[half][1];
             if (u != 6) {
               const float2 t = *reinterpret_cast<const float2*>(st + s * DK + c);
-              x *= D[half][0];
-              y *= D[half][1];
               D[half][0] *= t.x;
               D[half][1] *= t.y;
             }
-            split2(x, y, Bh[half], Bl[half]);
+            split2(kj.x, kj.y, Bh[half], Bl[half]);
           }
           const uint32_t* ah = u == 6 ? Rh : Ah;
           const uint32_t* al = u == 6 ? Rl : Al;
           const uint32_t* aq = u == 6 ? Rq : Aq;
-          mma(accA[uu], ah, Bh[0], Bh[1]);
-          mma(accB[uu], aq, Bh[0], Bh[1]);
-          mma(accA[uu], al, Bh[0], Bh[1]);
-          mma(accA[uu], ah, Bl[0], Bl[1]);
+          mma(accA[u], ah, Bh[0], Bh[1]);
+          mma(accB[u], aq, Bh[0], Bh[1]);
+          mma(accA[u], al, Bh[0], Bh[1]);
+          mma(accA[u], ah, Bl[0], Bl[1]);
         }
       }
     }
   }
-  __syncthreads();  // the operands are read: the matrices take their place
-  for (int i = tid; i < 3 * C::kMat / 16; i += 256) reinterpret_cast<float4*>(dsm)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  __syncthreads();  // the operands are read: the matrices and v take their place
+  for (int i = tid; i < 2 * C::kMat / 16; i += 256) reinterpret_cast<float4*>(dsm + C::oA)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = tid; i < kDeltaChunk * p.dv / 4; i += 256) {
+    const int r = i / (p.dv / 4), c = 4 * (i % (p.dv / 4));
+    unsigned int x[2] = {0u, 0u};
+    if (r < len) {
+      const __nv_bfloat16* src = p.v + (long long)(start + r) * p.v_t + h * p.v_h + c;
+      if (p.vec_v) {
+        x[0] = *reinterpret_cast<const uint32_t*>(src), x[1] = *reinterpret_cast<const uint32_t*>(src + 2);
+      } else {
+        const unsigned short* e = reinterpret_cast<const unsigned short*>(src);
+        x[0] = e[0] | (uint32_t)e[1] << 16, x[1] = e[2] | (uint32_t)e[3] << 16;
+      }
+    }
+    *reinterpret_cast<uint2*>(dsm + C::oV + r * C::kVRow + 2 * c) = make_uint2(x[0], x[1]);
+  }
   __syncthreads();
   constexpr float kUn = 1.f / (kOpScale * kOpScale);
 #pragma unroll 1
   for (int turn = 0; turn < 2; ++turn) {
     if (hh == turn) {
 #pragma unroll
-      for (int uu = 0; uu < 7; ++uu) {
-        const int s = uu == 6 ? 2 * ta : 2 * ta - 1 - uu;
+      for (int u = 0; u < 7; ++u) {
+        const int s = u == 6 ? 2 * ta : 2 * ta - 1 - u;
         if (s < 0) continue;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int r = 16 * ta + gq + (e >= 2 ? 8 : 0), c = 8 * s + 2 * tq + (e & 1);
-          if (uu == 6 && e < 2) continue;
-          mA[r * C::kMRow + c] += accA[uu][e] * (kUn * sbeta[r]);
-          mB[r * C::kMRow + c] += accB[uu][e] * kUn;
+          if (u == 6 && e < 2) continue;
+          mA[r * C::kMRow + c] += accA[u][e] * (kUn * sbeta[r]);
+          mB[r * C::kMRow + c] += accB[u][e] * kUn;
         }
       }
     }
@@ -734,9 +791,9 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
     __syncthreads();
   }
 
-  // ---- T = (I + A)^-1: 16 x 16 blocks on the diagonal by substitution, one
-  // column per lane, then the blocks below, diagonal by diagonal
-  if (warp < 4 && lane < 16) {
+  // ---- warps 0-3: the inverses of I + A's 16 x 16 diagonal blocks by substitution, a
+  // column per lane, in the blocks' place; warps 4-7: B to the record
+  if (warp < 4) {
     const int b = 16 * warp;
     float x[16];
 #pragma unroll
@@ -745,102 +802,177 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
 #pragma unroll
       for (int m = 0; m < i; ++m) y = fmaf(-mA[(b + i) * C::kMRow + b + m], x[m], y);
       x[i] = y;
-      mT[(b + i) * C::kMRow + b + lane] = y;
+    }
+    __syncwarp();
+    if (lane < 16) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) mA[(b + i) * C::kMRow + b + lane] = x[i];
+    }
+  } else {
+    unsigned char* out = rec + 5 * delta_tile_bytes(DK);
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const int i = n * 128 + tid - 128, r = i >> 3, piece = i & 7;
+      const float4 x = *reinterpret_cast<const float4*>(mB + r * C::kMRow + 8 * piece);
+      const float4 y = *reinterpret_cast<const float4*>(mB + r * C::kMRow + 8 * piece + 4);
+      *reinterpret_cast<uint4*>(out + r * 128 + ((piece ^ (r & 7)) << 4)) =
+          make_uint4(pack_half2(x.x * kOpScale, x.y * kOpScale), pack_half2(x.z * kOpScale, x.w * kOpScale),
+                     pack_half2(y.x * kOpScale, y.y * kOpScale), pack_half2(y.z * kOpScale, y.w * kOpScale));
     }
   }
   __syncthreads();
-#pragma unroll 1
-  for (int d = 1; d < 4; ++d) {
-    // block (bi, bi - d): 64 threads, 4 columns each
-    const int bi = d + (tid >> 6), bj = bi - d;
-    const int i = (tid & 63) >> 2, j = 4 * (tid & 3);
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (bi < 4) {
-      for (int m = 16 * bj; m < 16 * bi; ++m) {
-        const float x = mA[(16 * bi + i) * C::kMRow + m];
-        const float4 t = *reinterpret_cast<const float4*>(mT + m * C::kMRow + 16 * bj + j);
-        y.x = fmaf(x, t.x, y.x), y.y = fmaf(x, t.y, y.y), y.z = fmaf(x, t.z, y.z), y.w = fmaf(x, t.w, y.w);
-      }
-    }
-    // A T of the block goes above the diagonal, to block (bj, bi), which nothing reads
-    if (bi < 4) *reinterpret_cast<float4*>(mA + (16 * bj + i) * C::kMRow + 16 * bi + j) = y;
-    __syncthreads();
-    if (bi < 4) {
-      y = make_float4(0.f, 0.f, 0.f, 0.f);
+  // ---- A below the diagonal and the inverses on it as two fp16 terms
 #pragma unroll
-      for (int m = 0; m < 16; ++m) {
-        const float x = -mT[(16 * bi + i) * C::kMRow + 16 * bi + m];
-        const float4 t = *reinterpret_cast<const float4*>(mA + (16 * bj + m) * C::kMRow + 16 * bi + j);
-        y.x = fmaf(x, t.x, y.x), y.y = fmaf(x, t.y, y.y), y.z = fmaf(x, t.z, y.z), y.w = fmaf(x, t.w, y.w);
-      }
-      *reinterpret_cast<float4*>(mT + (16 * bi + i) * C::kMRow + 16 * bj + j) = y;
-    }
-    __syncthreads();
+  for (int n = 0; n < 2; ++n) {
+    const int i = n * 256 + tid, r = i >> 3, piece = i & 7;
+    const float4 x = *reinterpret_cast<const float4*>(mA + r * C::kMRow + 8 * piece);
+    const float4 y = *reinterpret_cast<const float4*>(mA + r * C::kMRow + 8 * piece + 4);
+    uint32_t hi[4], lo[4];
+    split2(x.x * kOpScale, x.y * kOpScale, hi[0], lo[0]);
+    split2(x.z * kOpScale, x.w * kOpScale, hi[1], lo[1]);
+    split2(y.x * kOpScale, y.y * kOpScale, hi[2], lo[2]);
+    split2(y.z * kOpScale, y.w * kOpScale, hi[3], lo[3]);
+    unsigned char* dst = dsm + C::oA16 + r * 128 + ((piece ^ (r & 7)) << 4);
+    *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(dst + 8192) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
-  // ---- T diag(b) and B to the record
-  {
-    const int r = tid >> 2;
-    unsigned char* out = rec + 3 * delta_tile_bytes(DK);
+  __syncthreads();
+
+  // ---- the solution, 16 columns of W or U~ at a time
+  const uint32_t a16 = smem_u32(dsm + C::oA16);
+  const int brow = (lane & 7) + ((lane >> 4) << 3), bpc = (lane >> 3) & 1;  // ldmatrix rows and pieces of a 16 x 16 block
+#pragma unroll 1
+  for (int tile = warp; tile < (DK + p.dv) / 16; tile += 8) {
+    const bool is_w = tile < DK / 16;
+    const int c = 16 * (is_w ? tile : tile - DK / 16) + gq;  // column of rows 0, 1 of the accumulators; + 8 of 2, 3
+    uint32_t fh[3][4], fl[3][4];
+    float f[3][2];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int piece = 2 * (tid & 3) + half, c = 8 * piece;
-      uint32_t hi[4], lo[4], bw[4];
+    for (int i = 0; i < 4; ++i) {
+      float y[2][4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 t = *reinterpret_cast<const float2*>(mT + r * C::kMRow + c + 2 * e);
-        const float2 b = *reinterpret_cast<const float2*>(mB + r * C::kMRow + c + 2 * e);
-        split2(t.x * sbeta[c + 2 * e] * kOpScale, t.y * sbeta[c + 2 * e + 1] * kOpScale, hi[e], lo[e]);
-        bw[e] = pack_half2(b.x * kOpScale, b.y * kOpScale);
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int n = 16 * i + 8 * nt + 2 * tq + (e & 1), cc = c + (e >= 2 ? 8 : 0);
+          const float x = is_w ? skp[n * C::kFRow + cc] * sbefore[(2 * i + nt) * DK + cc]
+                               : __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(dsm + C::oV + n * C::kVRow + 2 * cc));
+          y[nt][e] = x * sbeta[n];
+        }
+      uint32_t bh[4], bl[4];
+#pragma unroll
+      for (int j = 0; j < i; ++j) {
+        const uint32_t at = a16 + (16 * i + brow) * 128 + (((2 * j + bpc) ^ (brow & 7)) << 4);
+        ldsm_a(at, bh);
+        ldsm_a(at + 8192, bl);
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          float d[4] = {0.f, 0.f, 0.f, 0.f};
+          mma(d, fh[j], bh[2 * nt], bh[2 * nt + 1]);
+          mma(d, fl[j], bh[2 * nt], bh[2 * nt + 1]);
+          mma(d, fh[j], bl[2 * nt], bl[2 * nt + 1]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[nt][e] = fmaf(-f[j][e >> 1], d[e], y[nt][e]);
+        }
       }
-      const size_t at = (size_t)r * 128 + ((piece ^ (r & 7)) * 16);
-      *reinterpret_cast<uint4*>(out + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      *reinterpret_cast<uint4*>(out + 8192 + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      *reinterpret_cast<uint4*>(out + 16384 + at) = make_uint4(bw[0], bw[1], bw[2], bw[3]);
+      float s0, s1, i0, i1;
+      uint32_t yh[4], yl[4];
+      block_scale(quad_max(fmaxf(fmaxf(fabsf(y[0][0]), fabsf(y[0][1])), fmaxf(fabsf(y[1][0]), fabsf(y[1][1])))), s0, i0);
+      block_scale(quad_max(fmaxf(fmaxf(fabsf(y[0][2]), fabsf(y[0][3])), fmaxf(fabsf(y[1][2]), fabsf(y[1][3])))), s1, i1);
+      split_frag(y[0], y[1], s0, s1, yh, yl);
+      const uint32_t at = a16 + (16 * i + brow) * 128 + (((2 * i + bpc) ^ (brow & 7)) << 4);
+      ldsm_a(at, bh);
+      ldsm_a(at + 8192, bl);
+      float w[2][4];
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+        mma(d, yh, bh[2 * nt], bh[2 * nt + 1]);
+        mma(d, yl, bh[2 * nt], bh[2 * nt + 1]);
+        mma(d, yh, bl[2 * nt], bl[2 * nt + 1]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[nt][e] = d[e] * ((e >= 2 ? i1 : i0) * (1.f / kOpScale));
+      }
+      // the block as the next ones' operand; W's terms are the record's
+      uint32_t oh[4], ol[4];
+      if (is_w) {
+        s0 = s1 = kOpScale;
+        i0 = i1 = 1.f / kOpScale;
+      } else {
+        block_scale(quad_max(fmaxf(fmaxf(fabsf(w[0][0]), fabsf(w[0][1])), fmaxf(fabsf(w[1][0]), fabsf(w[1][1])))), s0, i0);
+        block_scale(quad_max(fmaxf(fmaxf(fabsf(w[0][2]), fabsf(w[0][3])), fmaxf(fabsf(w[1][2]), fabsf(w[1][3])))), s1, i1);
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+          *reinterpret_cast<float4*>(rec + delta_ops_bytes(DK) + ((((tile - DK / 16) * 8 + 2 * i + nt) * 32 + lane) << 4)) =
+              make_float4(w[nt][0], w[nt][1], w[nt][2], w[nt][3]);
+      }
+      split_frag(w[0], w[1], s0, s1, oh, ol);
+      if (is_w) {
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {  // rows c, c + 8; pieces 2 i, 2 i + 1 of 8 tokens
+          const int cc = c + 8 * (m & 1), piece = 2 * i + (m >> 1);
+          unsigned char* dst = rec + cc * 128 + ((piece ^ (cc & 7)) << 4) + 4 * tq;
+          *reinterpret_cast<uint32_t*>(dst) = oh[m];
+          *reinterpret_cast<uint32_t*>(dst + delta_tile_bytes(DK)) = ol[m];
+        }
+      }
+      if (i < 3) {
+#pragma unroll
+        for (int m = 0; m < 4; ++m) fh[i][m] = oh[m], fl[i][m] = ol[m];
+        f[i][0] = i0 * (1.f / kOpScale);
+        f[i][1] = i1 * (1.f / kOpScale);
+      }
     }
   }
 }
 
 // ---------------------------------------------------------------- prefill: the chain of chunks
-// One CTA per sequence, head and 32 state columns, the state in the
-// accumulators of its warps (warp w: rows 16 w ..).  Per chunk three products
-// in a row, with a barrier after each operand has been written: X from the
-// state, U from X, the new state from U; the output hangs beside them.  The
-// records arrive by bulk copies ahead of use: the first piece (k exp G, q exp G)
-// into one buffer that is free after X, the others into two buffers each.
-template <int DK>
+// One CTA per sequence, head and 16 MT state columns; two warps per 16 columns.
+// Everything is transposed, so that what one product leaves in its accumulators
+// is the next one's A operand in the same registers:
+//   U^T = U~^T - S^T W^T,  O^T = S^T (q exp G)^T + U^T B^T,
+//   S^T = S^T diag(exp G_last) + U^T (k exp(G_last - G)).
+// Of the pair, warp hf holds the channels' half hf of S^T and forms the tokens'
+// half hf of U^T and O^T; the halves of S^T and U^T go to the other warp as
+// operands through shared memory, with a barrier of the two each.  Operands are
+// two fp16 terms, a power of two per state column and half.  One more warp
+// brings the records, two ahead, by bulk copies.
+// The tensor cores' fp16 rate bounds it where there are sequences and heads
+// enough, the chain of mma.sync and exchanges of one chunk where there are few.
+template <int DK, int MT>
 struct ScanCfg {
-  static constexpr int kKq = 3 * delta_tile_bytes(DK);
-  static constexpr int kTa = delta_ta_bytes(DK);
-  static constexpr int kKh = 2 * delta_tile_bytes(DK);
-  static constexpr int oKq = 0, oTa = kKq, oKh = oTa + 2 * kTa;
-  static constexpr int kSt = DK * kDeltaCols * 2, kXt = kDeltaChunk * kDeltaCols * 2;
-  static constexpr int oS = oKh + 2 * kKh, oX = oS + 2 * kSt, oU = oX + 2 * kXt;
-  static constexpr int oSc = oU + 2 * kXt;           // scales: state [8], X [4][2], U [4][2]
-  static constexpr int oBar = oSc + 24 * 4, oInfo = oBar + 5 * 8;
-  static constexpr int kSmem = oInfo + 24;
+  static constexpr int kWarps = 2 * MT;
+  static constexpr int kThreads = 32 * kWarps + 32;
+  static constexpr int kOps = delta_ops_bytes(DK);
+  static constexpr int kKs = DK / 32;                      // 16-channel steps of a half
+  static constexpr int kXS = 2 * kKs * 2 * 512;            // a column tile's S^T operand: halves, steps, terms
+  static constexpr int kXU = 2 * 2 * 2 * 512;              // its U^T operand
+  static constexpr int oX = 2 * kOps, oU = oX + MT * kXS;
+  static constexpr int oFs = oU + MT * kXU, oFu = oFs + MT * 2 * 16 * 4;  // inverse scales [MT][half][16]
+  static constexpr int oBar = oFu + MT * 2 * 16 * 4, oInfo = oBar + 4 * 8;
+  static constexpr int kSmem = oInfo + 32;
 };
-// byte of (row, 16-byte piece) in a [rows][32] fp16 tile
-__device__ __forceinline__ int tile32(int row, int piece) { return row * 64 + ((piece ^ ((row >> 1) & 3)) << 4); }
 
-template <int DK>
-__global__ void __launch_bounds__(256, 1) delta_scan_kernel(const DeltaParams p) {
-  using C = ScanCfg<DK>;
-  constexpr int NB = DK / 16;  // 16-row blocks of the state
+template <int DK, int MT>
+__global__ void __launch_bounds__(ScanCfg<DK, MT>::kThreads, 1) delta_scan_kernel(const DeltaParams p) {
+  using C = ScanCfg<DK, MT>;
+  constexpr int KS = C::kKs, NT = 2 * KS, KT = delta_tile_bytes(DK);
   extern __shared__ __align__(128) unsigned char dsm[];
-  float* sc_s = reinterpret_cast<float*>(dsm + C::oSc);
-  float* sc_x = sc_s + 8;
-  float* sc_u = sc_x + 8;
-  uint64_t* bar = reinterpret_cast<uint64_t*>(dsm + C::oBar);  // kq, ta 0, ta 1, kh 0, kh 1
+  uint64_t* full = reinterpret_cast<uint64_t*>(dsm + C::oBar);
+  uint64_t* empty = full + 2;
   int* info = reinterpret_cast<int*>(dsm + C::oInfo);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int splits = p.dv / kDeltaCols;
+  const int splits = p.dv / (16 * MT);
   const int split = blockIdx.x % splits, h = blockIdx.x / splits % p.Hv, seq = blockIdx.x / splits / p.Hv;
   if (warp == 0) {
     int first, start, end;
     find_sequence(p, seq, first, start, end);
     if (lane == 0) {
       info[0] = first, info[1] = start, info[2] = end, info[3] = slot_of(p, seq);
-      for (int i = 0; i < 5; ++i) mbar_init(bar + i, 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(full + i, 1);
+        mbar_init(empty + i, C::kWarps);
+      }
       fence_mbar_init();
     }
   }
@@ -850,273 +982,230 @@ __global__ void __launch_bounds__(256, 1) delta_scan_kernel(const DeltaParams p)
   const int c0 = max(first, p.seg0), c1 = min(first + chunks, p.seg0 + p.seg_chunks);
   if (slot < 0 || c0 >= c1) return;
   const int n = c1 - c0;
-  const unsigned char* rec0 = p.ws + ((size_t)(c0 - p.seg0) * p.Hv + h) * delta_rec_bytes(DK);
-  const size_t rec_step = (size_t)p.Hv * delta_rec_bytes(DK);
-  const bool copies = tid == 0 && !p.skip;
-  auto issue_kq = [&](int c) {
-    mbar_arrive_expect_tx(bar, C::kKq);
-    bulk_g2s(dsm + C::oKq, rec0 + c * rec_step, C::kKq, bar);
-  };
-  auto issue_rest = [&](int c) {
-    const int b = c & 1;
-    mbar_arrive_expect_tx(bar + 1 + b, C::kTa);
-    bulk_g2s(dsm + C::oTa + b * C::kTa, rec0 + c * rec_step + C::kKq, C::kTa, bar + 1 + b);
-    mbar_arrive_expect_tx(bar + 3 + b, C::kKh);
-    bulk_g2s(dsm + C::oKh + b * C::kKh, rec0 + c * rec_step + C::kKq + C::kTa, C::kKh, bar + 3 + b);
-  };
-  if (copies) {
-    issue_kq(0);
-    issue_rest(0);
-    if (n > 1) issue_rest(1);
+  const unsigned char* rec0 = p.ws + ((size_t)(c0 - p.seg0) * p.Hv + h) * delta_rec_bytes(DK, p.dv);
+  const size_t rec_step = (size_t)p.Hv * delta_rec_bytes(DK, p.dv);
+
+  if (warp == C::kWarps) {  // the records
+    if (lane == 0 && !p.skip) {
+      int c = 0;
+      for (; c < n; ++c) {
+        const int b = c & 1;
+        if (c >= 2 && !mbar_wait(empty + b, ((c >> 1) & 1) ^ 1, p.wait_ns, p.err)) break;
+        mbar_arrive_expect_tx(full + b, C::kOps);
+        bulk_g2s(dsm + b * C::kOps, rec0 + c * rec_step, C::kOps, full + b);
+      }
+      // the CTA's shared memory stays until every copy has landed
+      for (int i = max(0, c - 2); i < c; ++i) mbar_wait(full + (i & 1), (i >> 1) & 1, kLandNs, p.err);
+    }
+    return;
   }
 
+  const int mt = warp >> 1, hf = warp & 1;
   const int gq = lane >> 2, tq = lane & 3;
-  const int col0 = split * kDeltaCols;
-  float* sp = p.state + ((size_t)slot * p.Hv + h) * DK * p.dv + col0;
-  float S[4][4];
+  const int col = (split * MT + mt) * 16;  // state columns col .. + 15; this lane's col + gq and + 8
+  float* sp = p.state + (((size_t)slot * p.Hv + h) * DK + hf * (DK / 2) + 2 * tq) * p.dv + col + gq;
+  float S[NT][4];  // S^T: rows the columns, channels 8 nt + 2 tq, + 1 of the half
   const bool zero = c0 == first && p.fresh && p.fresh[seq];
 #pragma unroll
-  for (int nt = 0; nt < 4; ++nt)
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int hi = 0; hi < 2; ++hi) {
-      float2 v = make_float2(0.f, 0.f);
-      if (warp < NB && !zero)
-        v = *reinterpret_cast<const float2*>(sp + (size_t)(16 * warp + gq + 8 * hi) * p.dv + 8 * nt + 2 * tq);
-      S[nt][2 * hi] = v.x;
-      S[nt][2 * hi + 1] = v.y;
-    }
-  const int ta = warp & 3, half = warp >> 2;  // row tile and column half of X, U and the output
-  // v of rows 16 ta + gq (+ 8), columns 16 half + 8 nt + 2 tq; zeros past the sequence
-  auto load_v = [&](int c, float v[2][4]) {
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-      for (int hi = 0; hi < 2; ++hi) {
-        const int t = start + (c0 - first + c) * kDeltaChunk + 16 * ta + gq + 8 * hi;
-        float x = 0.f, y = 0.f;
-        if (t < end) {
-          const __nv_bfloat16* src = p.v + (long long)t * p.v_t + h * p.v_h + col0 + 16 * half + 8 * nt + 2 * tq;
-          if (p.vec_v) {
-            const uint32_t r = *reinterpret_cast<const uint32_t*>(src);
-            x = bf16lo(r);
-            y = bf16hi(r);
-          } else {
-            x = __bfloat162float(src[0]);
-            y = __bfloat162float(src[1]);
-          }
-        }
-        v[nt][2 * hi] = x;
-        v[nt][2 * hi + 1] = y;
-      }
-  };
-  float v[2][4];
-  load_v(0, v);
+    for (int e = 0; e < 4; ++e) S[nt][e] = zero ? 0.f : sp[(size_t)(8 * nt + (e & 1)) * p.dv + (e >= 2 ? 8 : 0)];
+  uint4* xs = reinterpret_cast<uint4*>(dsm + C::oX + mt * C::kXS);  // [half][step][term][lane]
+  uint4* xu = reinterpret_cast<uint4*>(dsm + C::oU + mt * C::kXU);
+  float* fs = reinterpret_cast<float*>(dsm + C::oFs) + mt * 32;
+  float* fu = reinterpret_cast<float*>(dsm + C::oFu) + mt * 32;
+  auto pair_sync = [&] { asm volatile("bar.sync %0, 64;" :: "r"(mt + 1) : "memory"); };
   bool dead = false;  // a wait ran out: no further waits, the results are void
-  auto wait = [&](uint64_t* b, uint32_t parity) {
-    if (!dead) dead = !mbar_wait(b, parity, p.wait_ns, p.err);
-  };
+  // U~ of this warp's tokens: 4 tiles of 8
+  const unsigned char* ut = rec0 + C::kOps + (((size_t)(split * MT + mt) * 8 + 4 * hf) * 32 + lane) * 16;
+  float4 un[4];
+#pragma unroll
+  for (int nt = 0; nt < 4; ++nt) un[nt] = __ldcg(reinterpret_cast<const float4*>(ut + nt * 512));
   const uint32_t base = smem_u32(dsm);
-  const int arow = 16 * ta + (lane & 15), apc = lane >> 4;  // ldmatrix rows and pieces of an A tile
-  const int brow = lane & 15, bpc = 2 * half + (lane >> 4);  // of a B tile's 16 rows, this half's columns
+  const int trow = (lane & 7) + (lane & 8), tpc = lane >> 4;                // ldmatrix.trans of a 16 (k) x 16 (n) block
+  const int brow = (lane & 7) + ((lane >> 4) << 3), bpc = (lane >> 3) & 1;  // ldmatrix of a 16 (n) x 16 (k) block
 
 #pragma unroll 1
   for (int c = 0; c < n; ++c) {
     const int b = c & 1;
-    // ---- the state as two fp16 terms
-    if (warp < NB) {
-      float m = 0.f;
+    const uint32_t ops = base + b * C::kOps;
+    // ---- this half of S^T as operand
+    {
+      float m0 = 0.f, m1 = 0.f, s0, s1, i0, i1;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        m0 = fmaxf(m0, fmaxf(fabsf(S[nt][0]), fabsf(S[nt][1])));
+        m1 = fmaxf(m1, fmaxf(fabsf(S[nt][2]), fabsf(S[nt][3])));
+      }
+      block_scale(quad_max(m0), s0, i0);
+      block_scale(quad_max(m1), s1, i1);
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        uint32_t hi[4], lo[4];
+        split_frag(S[2 * ks], S[2 * ks + 1], s0, s1, hi, lo);
+        xs[((hf * KS + ks) * 2 + 0) * 32 + lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        xs[((hf * KS + ks) * 2 + 1) * 32 + lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+      if (tq == 0) {
+        fs[hf * 16 + gq] = i0 * (1.f / kOpScale);
+        fs[hf * 16 + gq + 8] = i1 * (1.f / kOpScale);
+      }
+    }
+    pair_sync();
+    if (!dead) dead = !mbar_wait(full + b, (c >> 1) & 1, p.wait_ns, p.err);
+    // ---- U^T and the state's part of O^T for this half of the tokens
+    float U[4][4], O[4][4];
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt) {
+      U[nt][0] = un[nt].x, U[nt][1] = un[nt].y, U[nt][2] = un[nt].z, U[nt][3] = un[nt].w;
+      O[nt][0] = O[nt][1] = O[nt][2] = O[nt][3] = 0.f;
+    }
+    if (c + 1 < n) {
+      ut += rec_step;
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt) un[nt] = __ldcg(reinterpret_cast<const float4*>(ut + nt * 512));
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      float d[4][4], o[4][4];
 #pragma unroll
       for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) m = fmaxf(m, fabsf(S[nt][e]));
-      float s, inv;
-      block_scale(warp_max_abs(m), s, inv);
-      if (lane == 0) sc_s[warp] = inv * (1.f / kOpScale);
+        for (int e = 0; e < 4; ++e) d[nt][e] = o[nt][e] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const uint4 h4 = xs[((half * KS + ks) * 2 + 0) * 32 + lane], l4 = xs[((half * KS + ks) * 2 + 1) * 32 + lane];
+        const uint32_t ah[4] = {h4.x, h4.y, h4.z, h4.w}, al[4] = {l4.x, l4.y, l4.z, l4.w};
+        uint32_t wh[2][4], wl[2][4], qh[2][4];
+        const int kr = 16 * (half * KS + ks);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {  // 16 tokens
+          const uint32_t wat = ops + (kr + trow) * 128 + (((4 * hf + 2 * g + tpc) ^ (trow & 7)) << 4);
+          ldsm_x4_t(wat, wh[g]);
+          ldsm_x4_t(wat + KT, wl[g]);
+          const int qr = 32 * hf + 16 * g + brow;
+          ldsm_a(ops + 2 * KT + qr * DK * 2 + (((kr / 8 + bpc) ^ (qr & 7)) << 4), qh[g]);
+        }
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) mma(d[nt], ah, wh[nt >> 1][2 * (nt & 1)], wh[nt >> 1][2 * (nt & 1) + 1]);
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) mma(o[nt], ah, qh[nt >> 1][2 * (nt & 1)], qh[nt >> 1][2 * (nt & 1) + 1]);
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) mma(d[nt], al, wh[nt >> 1][2 * (nt & 1)], wh[nt >> 1][2 * (nt & 1) + 1]);
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) mma(d[nt], ah, wl[nt >> 1][2 * (nt & 1)], wl[nt >> 1][2 * (nt & 1) + 1]);
+      }
+      const float f0 = fs[half * 16 + gq], f1 = fs[half * 16 + gq + 8];
 #pragma unroll
       for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
-        for (int hi = 0; hi < 2; ++hi) {
-          uint32_t xh, xl;
-          split2(S[nt][2 * hi] * s, S[nt][2 * hi + 1] * s, xh, xl);
-          const int at = tile32(16 * warp + gq + 8 * hi, nt) + 4 * tq;
-          *reinterpret_cast<uint32_t*>(dsm + C::oS + at) = xh;
-          *reinterpret_cast<uint32_t*>(dsm + C::oS + C::kSt + at) = xl;
+        for (int e = 0; e < 4; ++e) {
+          U[nt][e] = fmaf(-(e >= 2 ? f1 : f0), d[nt][e], U[nt][e]);
+          O[nt][e] = fmaf(e >= 2 ? f1 : f0, o[nt][e], O[nt][e]);
         }
     }
-    __syncthreads();
-    if (copies && c >= 1 && c + 1 < n) issue_rest(c + 1);
-    wait(bar, c & 1);
-    // ---- X = v - (k exp G) S, and (q exp G) S
-    float X[2][4], O[2][4];
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        X[nt][e] = v[nt][e];
-        O[nt][e] = 0.f;
-      }
-#pragma unroll
-    for (int ks = 0; ks < NB; ++ks) {
-      uint32_t kh[4], kl[4], qh[4], sh[4], sl[4];
-      const uint32_t aoff = base + C::oKq + arow * DK * 2 + (((2 * ks + apc) ^ (arow & 7)) << 4);
-      ldsm_a(aoff, kh);
-      ldsm_a(aoff + delta_tile_bytes(DK), kl);
-      ldsm_a(aoff + 2 * delta_tile_bytes(DK), qh);
-      const uint32_t boff = base + C::oS + tile32(16 * ks + brow, bpc);
-      ldsm_x4_t(boff, sh);
-      ldsm_x4_t(boff + C::kSt, sl);
-      const float f = sc_s[ks];
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        float d[4] = {0.f, 0.f, 0.f, 0.f}, e[4] = {0.f, 0.f, 0.f, 0.f};
-        mma(d, kh, sh[2 * nt], sh[2 * nt + 1]);
-        mma(e, qh, sh[2 * nt], sh[2 * nt + 1]);
-        mma(d, kl, sh[2 * nt], sh[2 * nt + 1]);
-        mma(d, kh, sl[2 * nt], sl[2 * nt + 1]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          X[nt][i] = fmaf(-f, d[i], X[nt][i]);
-          O[nt][i] = fmaf(f, e[i], O[nt][i]);
-        }
-      }
-    }
-    // a 16 x 16 block (rows 16 ta.., this column half) to shared memory as two terms
-    auto put = [&](const float x[2][4], int off, float* sc) {
-      float m = 0.f;
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) m = fmaxf(m, fabsf(x[nt][e]));
-      float s, inv;
-      block_scale(warp_max_abs(m), s, inv);
-      if (lane == 0) sc[2 * ta + half] = inv * (1.f / kOpScale);
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int hi = 0; hi < 2; ++hi) {
-          uint32_t xh, xl;
-          split2(x[nt][2 * hi] * s, x[nt][2 * hi + 1] * s, xh, xl);
-          const int at = tile32(16 * ta + gq + 8 * hi, 2 * half + nt) + 4 * tq;
-          *reinterpret_cast<uint32_t*>(dsm + off + at) = xh;
-          *reinterpret_cast<uint32_t*>(dsm + off + C::kXt + at) = xl;
-        }
-    };
-    put(X, C::oX, sc_x);
-    if (c + 1 < n) load_v(c + 1, v);
-    __syncthreads();
-    if (copies && c + 1 < n) issue_kq(c + 1);
-    wait(bar + 1 + b, (c >> 1) & 1);
-    // ---- U = T diag(b) X (T is lower triangular)
-    float U[2][4];
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) U[nt][e] = 0.f;
-    const uint32_t toff = base + C::oTa + b * C::kTa + arow * 128;
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      if (ks > ta) continue;
-      uint32_t th[4], tl[4], xh[4], xl[4];
-      ldsm_a(toff + (((2 * ks + apc) ^ (arow & 7)) << 4), th);
-      ldsm_a(toff + 8192 + (((2 * ks + apc) ^ (arow & 7)) << 4), tl);
-      const uint32_t boff = base + C::oX + tile32(16 * ks + brow, bpc);
-      ldsm_x4_t(boff, xh);
-      ldsm_x4_t(boff + C::kXt, xl);
-      const float f = sc_x[2 * ks + half];
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
-        mma(d, th, xh[2 * nt], xh[2 * nt + 1]);
-        mma(d, tl, xh[2 * nt], xh[2 * nt + 1]);
-        mma(d, th, xl[2 * nt], xl[2 * nt + 1]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) U[nt][i] = fmaf(f, d[i], U[nt][i]);
-      }
-    }
-    put(U, C::oU, sc_u);
-    __syncthreads();
-    wait(bar + 3 + b, (c >> 1) & 1);
-    // ---- S = diag(exp G_last) S + (k exp(G_last - G))^T U
-    if (warp < NB) {
-      const float* dec = reinterpret_cast<const float*>(dsm + C::oTa + b * C::kTa + 3 * 8192);
-      const float d0 = dec[16 * warp + gq], d1 = dec[16 * warp + gq + 8];
+    // ---- this half of U^T as operand
+    {
+      float m0 = 0.f, m1 = 0.f, s0, s1, i0, i1;
 #pragma unroll
       for (int nt = 0; nt < 4; ++nt) {
-        S[nt][0] *= d0;
-        S[nt][1] *= d0;
-        S[nt][2] *= d1;
-        S[nt][3] *= d1;
+        m0 = fmaxf(m0, fmaxf(fabsf(U[nt][0]), fabsf(U[nt][1])));
+        m1 = fmaxf(m1, fmaxf(fabsf(U[nt][2]), fabsf(U[nt][3])));
       }
+      block_scale(quad_max(m0), s0, i0);
+      block_scale(quad_max(m1), s1, i1);
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        uint32_t kh[4], kl[4];
-        const int row = 16 * ks + (lane & 7) + ((lane & 16) >> 1);
-        const uint32_t aoff =
-            base + C::oKh + b * C::kKh + row * DK * 2 + (((2 * warp + ((lane >> 3) & 1)) ^ (row & 7)) << 4);
-        ldsm_x4_t(aoff, kh);
-        ldsm_x4_t(aoff + delta_tile_bytes(DK), kl);
+      for (int ks = 0; ks < 2; ++ks) {
+        uint32_t hi[4], lo[4];
+        split_frag(U[2 * ks], U[2 * ks + 1], s0, s1, hi, lo);
+        xu[((hf * 2 + ks) * 2 + 0) * 32 + lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        xu[((hf * 2 + ks) * 2 + 1) * 32 + lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+      if (tq == 0) {
+        fu[hf * 16 + gq] = i0 * (1.f / kOpScale);
+        fu[hf * 16 + gq + 8] = i1 * (1.f / kOpScale);
+      }
+    }
+    pair_sync();
+    // ---- S^T of this half of the channels, O^T of this half of the tokens
+    const float* dec = reinterpret_cast<const float*>(dsm + b * C::kOps + 5 * KT + kDeltaChunk * kDeltaChunk * 2) +
+                       hf * (DK / 2) + 2 * tq;
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t uh[4], ul[4];
-          const uint32_t boff = base + C::oU + tile32(16 * ks + brow, 2 * hf + (lane >> 4));
-          ldsm_x4_t(boff, uh);
-          ldsm_x4_t(boff + C::kXt, ul);
-          const float f = sc_u[2 * ks + hf];
+    for (int nt = 0; nt < NT; ++nt) {
+      const float2 x = *reinterpret_cast<const float2*>(dec + 8 * nt);
+      S[nt][0] *= x.x, S[nt][1] *= x.y, S[nt][2] *= x.x, S[nt][3] *= x.y;
+    }
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt) {
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
-            mma(d, kh, uh[2 * nt], uh[2 * nt + 1]);
-            mma(d, kl, uh[2 * nt], uh[2 * nt + 1]);
-            mma(d, kh, ul[2 * nt], ul[2 * nt + 1]);
+    for (int half = 0; half < 2; ++half) {
+      float d[NT][4], o[4][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) S[2 * hf + nt][i] = fmaf(f, d[i], S[2 * hf + nt][i]);
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d[nt][e] = 0.f;
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[nt][e] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        const uint4 h4 = xu[((half * 2 + ks) * 2 + 0) * 32 + lane], l4 = xu[((half * 2 + ks) * 2 + 1) * 32 + lane];
+        const uint32_t ah[4] = {h4.x, h4.y, h4.z, h4.w}, al[4] = {l4.x, l4.y, l4.z, l4.w};
+        const int kr = 16 * (2 * half + ks);
+        uint32_t kh[KS][4];
+        const auto load_k = [&](uint32_t off) {
+#pragma unroll
+          for (int g = 0; g < KS; ++g)  // 16 channels
+            ldsm_x4_t(ops + off + (kr + trow) * DK * 2 + (((hf * (DK / 16) + 2 * g + tpc) ^ (trow & 7)) << 4), kh[g]);
+        };
+        load_k(3 * KT);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma(d[nt], ah, kh[nt >> 1][2 * (nt & 1)], kh[nt >> 1][2 * (nt & 1) + 1]);
+        if (half <= hf) {  // B is lower triangular
+          uint32_t bh[2][4];
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const int r = 32 * hf + 16 * g + brow;
+            ldsm_a(ops + 5 * KT + r * 128 + (((kr / 8 + bpc) ^ (r & 7)) << 4), bh[g]);
           }
+#pragma unroll
+          for (int nt = 0; nt < 4; ++nt) mma(o[nt], ah, bh[nt >> 1][2 * (nt & 1)], bh[nt >> 1][2 * (nt & 1) + 1]);
         }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma(d[nt], al, kh[nt >> 1][2 * (nt & 1)], kh[nt >> 1][2 * (nt & 1) + 1]);
+        load_k(4 * KT);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma(d[nt], ah, kh[nt >> 1][2 * (nt & 1)], kh[nt >> 1][2 * (nt & 1) + 1]);
       }
+      const float f0 = fu[half * 16 + gq], f1 = fu[half * 16 + gq + 8];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[nt][e] = fmaf(e >= 2 ? f1 : f0, d[nt][e], S[nt][e]);
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) O[nt][e] = fmaf(e >= 2 ? f1 : f0, o[nt][e], O[nt][e]);
     }
-    // ---- output: + B U (B is lower triangular with its diagonal)
+    __syncwarp();
+    if (lane == 0) mbar_arrive(empty + b);  // the record is read
+    // ---- out: 8 x 8 tiles turned, so that a lane has two columns of one token
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      if (ks > ta) continue;
-      uint32_t bh[4], uh[4];
-      ldsm_a(toff + 16384 + (((2 * ks + apc) ^ (arow & 7)) << 4), bh);
-      ldsm_x4_t(base + C::oU + tile32(16 * ks + brow, bpc), uh);
-      const float f = sc_u[2 * ks + half];
+    for (int nt = 0; nt < 4; ++nt) {
+      const int t = start + (c0 - first + c) * kDeltaChunk + 32 * hf + 8 * nt + gq;
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
-        mma(d, bh, uh[2 * nt], uh[2 * nt + 1]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) O[nt][i] = fmaf(f, d[i], O[nt][i]);
-      }
-    }
-#pragma unroll
-    for (int hi = 0; hi < 2; ++hi) {
-      const int t = start + (c0 - first + c) * kDeltaChunk + 16 * ta + gq + 8 * hi;
-      if (t < end) {
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-          *reinterpret_cast<__nv_bfloat162*>(p.out + ((size_t)t * p.Hv + h) * p.dv + col0 + 16 * half + 8 * nt + 2 * tq) =
-              __floats2bfloat162_rn(p.scale * O[nt][2 * hi], p.scale * O[nt][2 * hi + 1]);
+      for (int r = 0; r < 2; ++r) {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(p.scale * O[nt][2 * r], p.scale * O[nt][2 * r + 1]);
+        uint32_t y;
+        asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(*reinterpret_cast<const uint32_t*>(&x)));
+        if (t < end)
+          *reinterpret_cast<uint32_t*>(p.out + ((size_t)t * p.Hv + h) * p.dv + col + 8 * r + 2 * tq) = y;
       }
     }
   }
-  // after a time-out copies may still be landing: wait for the last of each buffer
-  if (copies && dead) {
-    mbar_wait(bar, (n - 1) & 1, kLandNs, p.err);
-    for (int c = max(0, n - 2); c < n; ++c) {
-      mbar_wait(bar + 1 + (c & 1), (c >> 1) & 1, kLandNs, p.err);
-      mbar_wait(bar + 3 + (c & 1), (c >> 1) & 1, kLandNs, p.err);
-    }
-  }
-  if (warp < NB) {
 #pragma unroll
-    for (int nt = 0; nt < 4; ++nt)
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int hi = 0; hi < 2; ++hi)
-        *reinterpret_cast<float2*>(sp + (size_t)(16 * warp + gq + 8 * hi) * p.dv + 8 * nt + 2 * tq) =
-            make_float2(S[nt][2 * hi], S[nt][2 * hi + 1]);
-  }
+    for (int e = 0; e < 4; ++e) sp[(size_t)(8 * nt + (e & 1)) * p.dv + (e >= 2 ? 8 : 0)] = S[nt][e];
 }
 
 // ---------------------------------------------------------------- host
@@ -1128,7 +1217,9 @@ static cudaError_t setup_dk() {
     e = cudaFuncSetAttribute(delta_step_kernel<DK, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              step_smem<DK>(128, true));
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(delta_scan_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, ScanCfg<DK>::kSmem);
+    e = cudaFuncSetAttribute(delta_scan_kernel<DK, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, ScanCfg<DK, 2>::kSmem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(delta_scan_kernel<DK, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize, ScanCfg<DK, 4>::kSmem);
   return e;
 }
 cudaError_t setup_delta() {
@@ -1170,12 +1261,20 @@ cudaError_t launch_delta_prep(const DeltaParams& p, int dk, cudaStream_t s) {
     delta_prep_kernel<128><<<grid, 256, PrepCfg<128>::kSmem, s>>>(p);
   return cudaGetLastError();
 }
-cudaError_t launch_delta_scan(const DeltaParams& p, int dk, cudaStream_t s) {
-  const unsigned grid = (unsigned)p.nseq * p.Hv * (p.dv / kDeltaCols);
+template <int DK, int MT>
+static void scan_launch(const DeltaParams& p, cudaStream_t s) {
+  using C = ScanCfg<DK, MT>;
+  delta_scan_kernel<DK, MT><<<(unsigned)p.nseq * p.Hv * (p.dv / (16 * MT)), C::kThreads, C::kSmem, s>>>(p);
+}
+// 32 state columns per CTA, the quickest chain, where that leaves an SM to each
+// CTA of the sequences that a segment may meet; otherwise 64, which read the
+// records half as often.
+cudaError_t launch_delta_scan(const DeltaParams& p, int dk, int sms, cudaStream_t s) {
+  const long long ctas = (long long)(p.nseq < p.seg_chunks ? p.nseq : p.seg_chunks) * p.Hv * (p.dv / 32);
   if (dk == 64)
-    delta_scan_kernel<64><<<grid, 256, ScanCfg<64>::kSmem, s>>>(p);
+    ctas <= sms ? scan_launch<64, 2>(p, s) : scan_launch<64, 4>(p, s);
   else
-    delta_scan_kernel<128><<<grid, 256, ScanCfg<128>::kSmem, s>>>(p);
+    ctas <= sms ? scan_launch<128, 2>(p, s) : scan_launch<128, 4>(p, s);
   return cudaGetLastError();
 }
 

@@ -10,13 +10,12 @@
 namespace lingmoe {
 
 constexpr int kDeltaChunk = 64;    // tokens per chunk of the prefill
-constexpr int kDeltaCols = 32;     // state columns per CTA
 constexpr int kDeltaMaxStep = 8;   // tokens per sequence of a step
 
-// one chunk of one head: what the scan needs of q, k, g and beta (delta.cu)
+// one chunk of one head: what the scan needs of q, k, v, g and beta (delta.cu)
 __host__ __device__ constexpr int delta_tile_bytes(int dk) { return kDeltaChunk * dk * 2; }
-__host__ __device__ constexpr int delta_ta_bytes(int dk) { return 3 * kDeltaChunk * kDeltaChunk * 2 + dk * 4; }
-__host__ __device__ constexpr int delta_rec_bytes(int dk) { return 5 * delta_tile_bytes(dk) + delta_ta_bytes(dk); }
+__host__ __device__ constexpr int delta_ops_bytes(int dk) { return 5 * delta_tile_bytes(dk) + kDeltaChunk * kDeltaChunk * 2 + dk * 4; }
+__host__ __device__ constexpr int delta_rec_bytes(int dk, int dv) { return delta_ops_bytes(dk) + kDeltaChunk * dv * 4; }
 
 struct DeltaParams {
   const __nv_bfloat16 *q, *k, *v;
@@ -45,6 +44,6 @@ struct DeltaParams {
 cudaError_t setup_delta();
 cudaError_t launch_delta_step(const DeltaParams& p, int dk, int sms, cudaStream_t s);
 cudaError_t launch_delta_prep(const DeltaParams& p, int dk, cudaStream_t s);
-cudaError_t launch_delta_scan(const DeltaParams& p, int dk, cudaStream_t s);
+cudaError_t launch_delta_scan(const DeltaParams& p, int dk, int sms, cudaStream_t s);
 
 }  // namespace lingmoe
