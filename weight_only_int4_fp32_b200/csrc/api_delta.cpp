@@ -190,7 +190,7 @@ int ling_moe_delta_prefill(ling_moe_delta_t* h, const ling_moe_delta_io_t* io, i
     p.seg0 = (int)c;
     p.seg_chunks = (int)(all - c < h->seg_chunks ? all - c : h->seg_chunks);
     cudaError_t e = launch_delta_prep(p, h->cfg.head_k, s);
-    if (e == cudaSuccess) e = launch_delta_scan(p, h->cfg.head_k, h->sms, s);
+    if (e == cudaSuccess) e = launch_delta_scan(p, h->cfg.head_k, s);
     if (e != cudaSuccess) return fail_cuda(e, "delta rule prefill launch");
     h->launches.fetch_add(2);
   }

@@ -121,21 +121,27 @@ __device__ __forceinline__ int slot_of(const DeltaParams& p, int seq) {
   return s >= 0 && s < p.num_slots ? s : -1;
 }
 
-// N consecutive channels of a bf16 row as floats
+// N consecutive channels of a bf16 row, two to a word; converted apart from the
+// load, so that a thread's loads are in flight together
 template <int N>
-__device__ __forceinline__ void load_bf16(const __nv_bfloat16* src, bool vec, float* x) {
+__device__ __forceinline__ void load_bf16(const __nv_bfloat16* src, bool vec, uint32_t* r) {
   if (vec) {
     if constexpr (N == 4) {
-      const uint2 r = *reinterpret_cast<const uint2*>(src);
-      x[0] = bf16lo(r.x), x[1] = bf16hi(r.x), x[2] = bf16lo(r.y), x[3] = bf16hi(r.y);
+      const uint2 x = *reinterpret_cast<const uint2*>(src);
+      r[0] = x.x, r[1] = x.y;
     } else {
-      const uint32_t r = *reinterpret_cast<const uint32_t*>(src);
-      x[0] = bf16lo(r), x[1] = bf16hi(r);
+      r[0] = *reinterpret_cast<const uint32_t*>(src);
     }
   } else {
+    const unsigned short* e = reinterpret_cast<const unsigned short*>(src);
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = __bfloat162float(src[i]);
+    for (int i = 0; i < N / 2; ++i) r[i] = e[2 * i] | (uint32_t)e[2 * i + 1] << 16;
   }
+}
+template <int N>
+__device__ __forceinline__ void from_bf16(const uint32_t* r, float* x) {
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) x[2 * i] = bf16lo(r[i]), x[2 * i + 1] = bf16hi(r[i]);
 }
 // N consecutive channels' log-decays (one for all where there is one per head)
 template <int N>
@@ -222,22 +228,27 @@ struct StepTokens {  // a head's tokens, prepared
 // what a lane loads of a token: CPL channels each of q, k and g, two or four of v
 template <int DK>
 struct StepRaw {
-  float q[DK / 32], k[DK / 32], g[DK / 32], v[4], beta;
+  uint32_t rq[DK / 64], rk[DK / 64], rv[2];
+  float g[DK / 32], beta;
   __device__ __forceinline__ void load(const DeltaParams& p, int b, int h, int t, int lane) {
     constexpr int CPL = DK / 32;
     const int hk = h / (p.Hv / p.Hk);
-    load_bf16<CPL>(p.q + b * p.q_b + t * p.q_t + hk * p.q_h + CPL * lane, p.vec_qk, q);
-    load_bf16<CPL>(p.k + b * p.k_b + t * p.k_t + hk * p.k_h + CPL * lane, p.vec_qk, k);
+    load_bf16<CPL>(p.q + b * p.q_b + t * p.q_t + hk * p.q_h + CPL * lane, p.vec_qk, rq);
+    load_bf16<CPL>(p.k + b * p.k_b + t * p.k_t + hk * p.k_h + CPL * lane, p.vec_qk, rk);
     load_decay<CPL>(p.g + b * p.g_b + t * p.g_t + h * p.g_h + p.g_c * CPL * lane, p.g_c, p.vec_g, g);
     const __nv_bfloat16* vp = p.v + b * p.v_b + t * p.v_t + h * p.v_h + 2 * lane;
-    load_bf16<2>(vp, p.vec_v, v);
-    if (p.dv > 64) load_bf16<2>(vp + 64, p.vec_v, v + 2);
+    load_bf16<2>(vp, p.vec_v, rv);
+    rv[1] = 0u;
+    if (p.dv > 64) load_bf16<2>(vp + 64, p.vec_v, rv + 1);
     beta = p.beta[b * p.be_b + t * p.be_t + h * p.be_h];
   }
   __device__ __forceinline__ void finish(StepTokens<DK>& s, int t, int lane) {
-    *reinterpret_cast<float2*>(&s.v[t][2 * lane]) = make_float2(v[0], v[1]);
-    *reinterpret_cast<float2*>(&s.v[t][2 * lane + 64]) = make_float2(v[2], v[3]);
+    *reinterpret_cast<float2*>(&s.v[t][2 * lane]) = make_float2(bf16lo(rv[0]), bf16hi(rv[0]));
+    *reinterpret_cast<float2*>(&s.v[t][2 * lane + 64]) = make_float2(bf16lo(rv[1]), bf16hi(rv[1]));
     constexpr int CPL = DK / 32;
+    float q[CPL], k[CPL];
+    from_bf16<CPL>(rq, q);
+    from_bf16<CPL>(rk, k);
     float qq = 0.f, kk = 0.f, kq = 0.f;
 #pragma unroll
     for (int c = 0; c < CPL; ++c) qq += q[c] * q[c], kk += k[c] * k[c];
@@ -431,9 +442,10 @@ __global__ void __launch_bounds__(256, 2) delta_step_kernel(const DeltaParams p)
 // blocks in registers (what a product leaves is the next one's operand), with the
 // inverses of the diagonal blocks formed by substitution before.
 //
-// The record of a chunk and head: W^T hi, lo [dk][64] | q exp(G) [64][dk] |
-// k exp(G_last - G) hi, lo [64][dk] | B [64][64] | exp(G_last) fp32 [dk] | U~^T fp32
-// in the order of the accumulators that take it.  fp16 rows have their 16-byte
+// The record of a chunk and head: W^T hi, lo in the order of the B operands that
+// it becomes | q exp(G) [64][dk] | k exp(G_last - G) hi, lo [64][dk] | B [64][64] |
+// exp(G_last) fp32 [dk] | U~^T fp32 in the order of the accumulators that take it.
+// fp16 rows have their 16-byte
 // pieces exchanged, piece ^= row % 8, for conflict-free ldmatrix.
 template <int DK>
 struct PrepCfg {
@@ -466,6 +478,12 @@ __device__ __forceinline__ void split_frag(const float x[4], const float y[4], f
   split2(y[0] * s0, y[1] * s0, hi[2], lo[2]);
   split2(y[2] * s1, y[3] * s1, hi[3], lo[3]);
 }
+// an 8 x 8 tile of 16-bit values, rows and columns exchanged
+__device__ __forceinline__ uint32_t turn8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 // the largest of a row, held by the four lanes of a quad
 __device__ __forceinline__ float quad_max(float m) {
   m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
@@ -486,10 +504,10 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
   float* mA = reinterpret_cast<float*>(dsm + C::oA);
   float* mB = reinterpret_cast<float*>(dsm + C::oBm);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int h = blockIdx.y, hk = h / (p.Hv / p.Hk);
+  const int h = blockIdx.x % p.Hv, hk = h / (p.Hv / p.Hk);
   if (warp == 0) {
     int seq = 0, start = 0, len = 0;
-    const bool ok = find_chunk(p, p.seg0 + blockIdx.x, seq, start, len) && slot_of(p, seq) >= 0;
+    const bool ok = find_chunk(p, p.seg0 + (int)(blockIdx.x / p.Hv), seq, start, len) && slot_of(p, seq) >= 0;
     if (lane == 0) {
       info[0] = ok ? len : 0;
       info[1] = start;
@@ -498,22 +516,30 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
   __syncthreads();
   const int len = info[0], start = info[1];
   if (len == 0) return;
-  unsigned char* rec = p.ws + ((size_t)blockIdx.x * p.Hv + h) * delta_rec_bytes(DK, p.dv);
+  unsigned char* rec = p.ws + (size_t)blockIdx.x * delta_rec_bytes(DK, p.dv);
 
   // ---- this warp's 8 rows, CPL channels per lane
   const int row0 = 8 * warp, c0 = CPL * lane;
   float q[8][CPL], k[8][CPL], a[8][CPL];
+  {
+    uint32_t rq[8][CPL / 2], rk[8][CPL / 2];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = row0 + i;
-    if (r < len) {
-      const long long t = start + r;
-      load_bf16<CPL>(p.q + t * p.q_t + hk * p.q_h + c0, p.vec_qk, q[i]);
-      load_bf16<CPL>(p.k + t * p.k_t + hk * p.k_h + c0, p.vec_qk, k[i]);
-      load_decay<CPL>(p.g + t * p.g_t + h * p.g_h + p.g_c * c0, p.g_c, p.vec_g, a[i]);
-    } else {  // past the sequence: no key, no query, no decay
+    for (int i = 0; i < 8; ++i) {
+      const int r = row0 + i;
+      if (r < len) {
+        const long long t = start + r;
+        load_bf16<CPL>(p.q + t * p.q_t + hk * p.q_h + c0, p.vec_qk, rq[i]);
+        load_bf16<CPL>(p.k + t * p.k_t + hk * p.k_h + c0, p.vec_qk, rk[i]);
+        load_decay<CPL>(p.g + t * p.g_t + h * p.g_h + p.g_c * c0, p.g_c, p.vec_g, a[i]);
+      } else {  // past the sequence: no key, no query, no decay
 #pragma unroll
-      for (int c = 0; c < CPL; ++c) q[i][c] = k[i][c] = a[i][c] = 0.f;
+        for (int c = 0; c < CPL; ++c) rq[i][c / 2] = rk[i][c / 2] = 0u, a[i][c] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      from_bf16<CPL>(rq[i], q[i]);
+      from_bf16<CPL>(rk[i], k[i]);
     }
   }
   if (lane < 8) {
@@ -743,19 +769,23 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
   }
   __syncthreads();  // the operands are read: the matrices and v take their place
   for (int i = tid; i < 2 * C::kMat / 16; i += 256) reinterpret_cast<float4*>(dsm + C::oA)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = tid; i < kDeltaChunk * p.dv / 4; i += 256) {
-    const int r = i / (p.dv / 4), c = 4 * (i % (p.dv / 4));
-    unsigned int x[2] = {0u, 0u};
-    if (r < len) {
-      const __nv_bfloat16* src = p.v + (long long)(start + r) * p.v_t + h * p.v_h + c;
-      if (p.vec_v) {
-        x[0] = *reinterpret_cast<const uint32_t*>(src), x[1] = *reinterpret_cast<const uint32_t*>(src + 2);
-      } else {
-        const unsigned short* e = reinterpret_cast<const unsigned short*>(src);
-        x[0] = e[0] | (uint32_t)e[1] << 16, x[1] = e[2] | (uint32_t)e[3] << 16;
+  {
+    uint32_t x[8][2];
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {  // 256 threads x 8 x 4 values: dv = 128
+      const int i = n * 256 + tid, r = i / (p.dv / 4), c = 4 * (i % (p.dv / 4));
+      x[n][0] = x[n][1] = 0u;
+      if (r < len) {
+        const __nv_bfloat16* src = p.v + (long long)(start + r) * p.v_t + h * p.v_h + c;
+        load_bf16<2>(src, p.vec_v, x[n]);
+        load_bf16<2>(src + 2, p.vec_v, x[n] + 1);
       }
     }
-    *reinterpret_cast<uint2*>(dsm + C::oV + r * C::kVRow + 2 * c) = make_uint2(x[0], x[1]);
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      const int i = n * 256 + tid, r = i / (p.dv / 4), c = 4 * (i % (p.dv / 4));
+      if (r < kDeltaChunk) *reinterpret_cast<uint2*>(dsm + C::oV + r * C::kVRow + 2 * c) = make_uint2(x[n][0], x[n][1]);
+    }
   }
   __syncthreads();
   constexpr float kUn = 1.f / (kOpScale * kOpScale);
@@ -907,14 +937,10 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
               make_float4(w[nt][0], w[nt][1], w[nt][2], w[nt][3]);
       }
       split_frag(w[0], w[1], s0, s1, oh, ol);
-      if (is_w) {
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {  // rows c, c + 8; pieces 2 i, 2 i + 1 of 8 tokens
-          const int cc = c + 8 * (m & 1), piece = 2 * i + (m >> 1);
-          unsigned char* dst = rec + cc * 128 + ((piece ^ (cc & 7)) << 4) + 4 * tq;
-          *reinterpret_cast<uint32_t*>(dst) = oh[m];
-          *reinterpret_cast<uint32_t*>(dst + delta_tile_bytes(DK)) = ol[m];
-        }
+      if (is_w) {  // 8 x 8 tiles turned: the B operand of 16 channels and tokens 16 i ..
+        uint4* dst = reinterpret_cast<uint4*>(rec) + (tile * 4 + i) * 32 + lane;
+        *dst = make_uint4(turn8(oh[0]), turn8(oh[1]), turn8(oh[2]), turn8(oh[3]));
+        dst[delta_tile_bytes(DK) / 16] = make_uint4(turn8(ol[0]), turn8(ol[1]), turn8(ol[2]), turn8(ol[3]));
       }
       if (i < 3) {
 #pragma unroll
@@ -927,7 +953,10 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
 }
 
 // ---------------------------------------------------------------- prefill: the chain of chunks
-// One CTA per sequence, head and 16 MT state columns; two warps per 16 columns.
+// One CTA per sequence, head and 32 state columns; two warps per 16 columns.
+// (64 columns per CTA read the records half as often, but a chunk then takes 4.5
+// us in place of 2.5: worth it only where many sequences share a segment, and
+// then by a tenth.)
 // Everything is transposed, so that what one product leaves in its accumulators
 // is the next one's A operand in the same registers:
 //   U^T = U~^T - S^T W^T,  O^T = S^T (q exp G)^T + U^T B^T,
@@ -939,8 +968,11 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
 // brings the records, two ahead, by bulk copies.
 // The tensor cores' fp16 rate bounds it where there are sequences and heads
 // enough, the chain of mma.sync and exchanges of one chunk where there are few.
-template <int DK, int MT>
+constexpr int kScanTiles = 2;  // 16-column tiles per CTA
+
+template <int DK>
 struct ScanCfg {
+  static constexpr int MT = kScanTiles;
   static constexpr int kWarps = 2 * MT;
   static constexpr int kThreads = 32 * kWarps + 32;
   static constexpr int kOps = delta_ops_bytes(DK);
@@ -953,10 +985,10 @@ struct ScanCfg {
   static constexpr int kSmem = oInfo + 32;
 };
 
-template <int DK, int MT>
-__global__ void __launch_bounds__(ScanCfg<DK, MT>::kThreads, 1) delta_scan_kernel(const DeltaParams p) {
-  using C = ScanCfg<DK, MT>;
-  constexpr int KS = C::kKs, NT = 2 * KS, KT = delta_tile_bytes(DK);
+template <int DK>
+__global__ void __launch_bounds__(ScanCfg<DK>::kThreads, 1) delta_scan_kernel(const DeltaParams p) {
+  using C = ScanCfg<DK>;
+  constexpr int MT = C::MT, KS = C::kKs, NT = 2 * KS, KT = delta_tile_bytes(DK);
   extern __shared__ __align__(128) unsigned char dsm[];
   uint64_t* full = reinterpret_cast<uint64_t*>(dsm + C::oBar);
   uint64_t* empty = full + 2;
@@ -1080,9 +1112,10 @@ __global__ void __launch_bounds__(ScanCfg<DK, MT>::kThreads, 1) delta_scan_kerne
         const int kr = 16 * (half * KS + ks);
 #pragma unroll
         for (int g = 0; g < 2; ++g) {  // 16 tokens
-          const uint32_t wat = ops + (kr + trow) * 128 + (((4 * hf + 2 * g + tpc) ^ (trow & 7)) << 4);
-          ldsm_x4_t(wat, wh[g]);
-          ldsm_x4_t(wat + KT, wl[g]);
+          const uint4* wat = reinterpret_cast<const uint4*>(dsm + b * C::kOps) + ((half * KS + ks) * 4 + 2 * hf + g) * 32 + lane;
+          const uint4 x = wat[0], y = wat[KT / 16];
+          wh[g][0] = x.x, wh[g][1] = x.y, wh[g][2] = x.z, wh[g][3] = x.w;
+          wl[g][0] = y.x, wl[g][1] = y.y, wl[g][2] = y.z, wl[g][3] = y.w;
           const int qr = 32 * hf + 16 * g + brow;
           ldsm_a(ops + 2 * KT + qr * DK * 2 + (((kr / 8 + bpc) ^ (qr & 7)) << 4), qh[g]);
         }
@@ -1195,8 +1228,7 @@ __global__ void __launch_bounds__(ScanCfg<DK, MT>::kThreads, 1) delta_scan_kerne
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const __nv_bfloat162 x = __floats2bfloat162_rn(p.scale * O[nt][2 * r], p.scale * O[nt][2 * r + 1]);
-        uint32_t y;
-        asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(*reinterpret_cast<const uint32_t*>(&x)));
+        const uint32_t y = turn8(*reinterpret_cast<const uint32_t*>(&x));
         if (t < end)
           *reinterpret_cast<uint32_t*>(p.out + ((size_t)t * p.Hv + h) * p.dv + col + 8 * r + 2 * tq) = y;
       }
@@ -1217,9 +1249,7 @@ static cudaError_t setup_dk() {
     e = cudaFuncSetAttribute(delta_step_kernel<DK, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              step_smem<DK>(128, true));
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(delta_scan_kernel<DK, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, ScanCfg<DK, 2>::kSmem);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(delta_scan_kernel<DK, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize, ScanCfg<DK, 4>::kSmem);
+    e = cudaFuncSetAttribute(delta_scan_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, ScanCfg<DK>::kSmem);
   return e;
 }
 cudaError_t setup_delta() {
@@ -1254,27 +1284,19 @@ cudaError_t launch_delta_step(const DeltaParams& p, int dk, int sms, cudaStream_
   return cudaGetLastError();
 }
 cudaError_t launch_delta_prep(const DeltaParams& p, int dk, cudaStream_t s) {
-  const dim3 grid((unsigned)p.seg_chunks, (unsigned)p.Hv);
+  const unsigned grid = (unsigned)p.seg_chunks * p.Hv;
   if (dk == 64)
     delta_prep_kernel<64><<<grid, 256, PrepCfg<64>::kSmem, s>>>(p);
   else
     delta_prep_kernel<128><<<grid, 256, PrepCfg<128>::kSmem, s>>>(p);
   return cudaGetLastError();
 }
-template <int DK, int MT>
-static void scan_launch(const DeltaParams& p, cudaStream_t s) {
-  using C = ScanCfg<DK, MT>;
-  delta_scan_kernel<DK, MT><<<(unsigned)p.nseq * p.Hv * (p.dv / (16 * MT)), C::kThreads, C::kSmem, s>>>(p);
-}
-// 32 state columns per CTA, the quickest chain, where that leaves an SM to each
-// CTA of the sequences that a segment may meet; otherwise 64, which read the
-// records half as often.
-cudaError_t launch_delta_scan(const DeltaParams& p, int dk, int sms, cudaStream_t s) {
-  const long long ctas = (long long)(p.nseq < p.seg_chunks ? p.nseq : p.seg_chunks) * p.Hv * (p.dv / 32);
+cudaError_t launch_delta_scan(const DeltaParams& p, int dk, cudaStream_t s) {
+  const unsigned grid = (unsigned)p.nseq * p.Hv * (p.dv / (16 * kScanTiles));
   if (dk == 64)
-    ctas <= sms ? scan_launch<64, 2>(p, s) : scan_launch<64, 4>(p, s);
+    delta_scan_kernel<64><<<grid, ScanCfg<64>::kThreads, ScanCfg<64>::kSmem, s>>>(p);
   else
-    ctas <= sms ? scan_launch<128, 2>(p, s) : scan_launch<128, 4>(p, s);
+    delta_scan_kernel<128><<<grid, ScanCfg<128>::kThreads, ScanCfg<128>::kSmem, s>>>(p);
   return cudaGetLastError();
 }
 
