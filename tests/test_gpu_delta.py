@@ -180,9 +180,10 @@ def test_prefill_matches_the_oracle(lengths, Hk, Hv, dk, dv, channel):
     f.close()
 
 
-@pytest.mark.parametrize("lengths", [[700], [100, 3, 597], [320, 0, 380]])
+@pytest.mark.parametrize("lengths", [[2500], [100, 3, 2397], [1152, 0, 1348], [1200, 1300]])
 def test_prefill_over_several_segments(lengths):
-    """64 heads: a segment of the workspace holds 10 chunks, so these take two."""
+    """64 heads: a segment of the workspace holds 18 chunks (8 records per SM), so these take three:
+    the halves of the workspace are used in turn, and again."""
     Hk, Hv, dk, dv, T, n = 32, 64, 64, 64, sum(lengths), len(lengths)
     f = lm.GatedDeltaRule(Hk, Hv, dk, dv, max_tokens=T, max_seqs=n)
     a = make(T, Hk, Hv, dk, dv, True, 4)
@@ -190,7 +191,7 @@ def test_prefill_over_several_segments(lengths):
     st0 = st.clone()
     cu = np.concatenate([[0], np.cumsum(lengths)])
     out = f.prefill(*a, st, torch.tensor(cu, dtype=torch.int32, device=DEV))
-    assert f.status() == lm.LING_MOE_OK and f.launch_count() >= 4
+    assert f.status() == lm.LING_MOE_OK and f.launch_count() >= 6
     for i in range(n):
         if not lengths[i]:
             continue

@@ -37,6 +37,8 @@ constexpr float kOpScale = 1024.f;  // k, q, T and B operands are stored times 2
 constexpr float kNormEps = 1e-6f;
 constexpr unsigned long long kLandNs = 2000000000ull;
 
+__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared.b64 _, [%0];" :: "r"(smem_u32(bar)) : "memory");
 }
@@ -505,6 +507,7 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
   float* mB = reinterpret_cast<float*>(dsm + C::oBm);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int h = blockIdx.x % p.Hv, hk = h / (p.Hv / p.Hk);
+  pdl_launch_dependents();
   if (warp == 0) {
     int seq = 0, start = 0, len = 0;
     const bool ok = find_chunk(p, p.seg0 + (int)(blockIdx.x / p.Hv), seq, start, len) && slot_of(p, seq) >= 0;
@@ -515,7 +518,14 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
   }
   __syncthreads();
   const int len = info[0], start = info[1];
-  if (len == 0) return;
+  // This kernel runs beside the scan before it, whose records are in the other
+  // half of the workspace.  It ends after that scan: the next one starts from its
+  // states, the next preparation writes to its half.
+  const bool last = blockIdx.x == gridDim.x - 1;
+  if (len == 0) {
+    if (last) pdl_wait();
+    return;
+  }
   unsigned char* rec = p.ws + (size_t)blockIdx.x * delta_rec_bytes(DK, p.dv);
 
   // ---- this warp's 8 rows, CPL channels per lane
@@ -950,6 +960,7 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
       }
     }
   }
+  if (last) pdl_wait();
 }
 
 // ---------------------------------------------------------------- prefill: the chain of chunks
@@ -1009,6 +1020,10 @@ __global__ void __launch_bounds__(ScanCfg<DK>::kThreads, 1) delta_scan_kernel(co
     }
   }
   __syncthreads();
+  // The records, and the states of the scan before.  Every CTA waits, those
+  // without work too: the next preparation may start once all have passed.
+  pdl_wait();
+  pdl_launch_dependents();
   const int first = info[0], start = info[1], end = info[2], slot = info[3];
   const int chunks = (end - start + kDeltaChunk - 1) / kDeltaChunk;
   const int c0 = max(first, p.seg0), c1 = min(first + chunks, p.seg0 + p.seg_chunks);
@@ -1283,21 +1298,32 @@ cudaError_t launch_delta_step(const DeltaParams& p, int dk, int sms, cudaStream_
     step_launch<128, false>(p, grid, warps, s);
   return cudaGetLastError();
 }
-cudaError_t launch_delta_prep(const DeltaParams& p, int dk, cudaStream_t s) {
+// launched while the kernel before it in the stream may still run (it waits for it itself)
+static cudaError_t launch_dependent(void (*kernel)(DeltaParams), unsigned grid, int threads, int smem, bool dependent,
+                                    cudaStream_t s, const DeltaParams& p) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(grid);
+  c.blockDim = dim3((unsigned)threads);
+  c.dynamicSmemBytes = (size_t)smem;
+  c.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = at;
+  c.numAttrs = dependent ? 1 : 0;
+  return cudaLaunchKernelEx(&c, kernel, p);
+}
+// The first preparation of a call follows what is before it in the stream; the
+// others run beside the scan before them.
+cudaError_t launch_delta_prep(const DeltaParams& p, int dk, bool first, cudaStream_t s) {
   const unsigned grid = (unsigned)p.seg_chunks * p.Hv;
-  if (dk == 64)
-    delta_prep_kernel<64><<<grid, 256, PrepCfg<64>::kSmem, s>>>(p);
-  else
-    delta_prep_kernel<128><<<grid, 256, PrepCfg<128>::kSmem, s>>>(p);
-  return cudaGetLastError();
+  if (dk == 64) return launch_dependent(delta_prep_kernel<64>, grid, 256, PrepCfg<64>::kSmem, !first, s, p);
+  return launch_dependent(delta_prep_kernel<128>, grid, 256, PrepCfg<128>::kSmem, !first, s, p);
 }
 cudaError_t launch_delta_scan(const DeltaParams& p, int dk, cudaStream_t s) {
   const unsigned grid = (unsigned)p.nseq * p.Hv * (p.dv / (16 * kScanTiles));
-  if (dk == 64)
-    delta_scan_kernel<64><<<grid, ScanCfg<64>::kThreads, ScanCfg<64>::kSmem, s>>>(p);
-  else
-    delta_scan_kernel<128><<<grid, ScanCfg<128>::kThreads, ScanCfg<128>::kSmem, s>>>(p);
-  return cudaGetLastError();
+  if (dk == 64) return launch_dependent(delta_scan_kernel<64>, grid, ScanCfg<64>::kThreads, ScanCfg<64>::kSmem, true, s, p);
+  return launch_dependent(delta_scan_kernel<128>, grid, ScanCfg<128>::kThreads, ScanCfg<128>::kSmem, true, s, p);
 }
 
 }  // namespace lingmoe

@@ -43,7 +43,7 @@ struct DeltaParams {
 
 cudaError_t setup_delta();
 cudaError_t launch_delta_step(const DeltaParams& p, int dk, int sms, cudaStream_t s);
-cudaError_t launch_delta_prep(const DeltaParams& p, int dk, cudaStream_t s);
+cudaError_t launch_delta_prep(const DeltaParams& p, int dk, bool first, cudaStream_t s);
 cudaError_t launch_delta_scan(const DeltaParams& p, int dk, cudaStream_t s);
 
 }  // namespace lingmoe
