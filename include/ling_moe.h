@@ -399,9 +399,10 @@ int ling_moe_fp8_linear_create(const uint8_t *codes, const float *scales, int ou
  * (bf16) on `stream`; rows x_stride and out_stride elements apart (at least a
  * row; not read for T <= 1), elements of a row contiguous, any alignment of the
  * element size (16-byte aligned rows are faster).  out must not overlap x.
- * 0 <= T <= max_tokens; T == 0 enqueues nothing.  Two launches (quantisation;
- * product: up to 8 tokens a weight-streaming kernel, more the tensor-core
- * tiles); asynchronous, no allocation, capturable.  Device-side failures (a
+ * 0 <= T <= max_tokens; T == 0 enqueues nothing.  Up to 8 tokens one launch of a
+ * weight-streaming kernel (two where their codes pass 104 KB: 8 tokens of some
+ * 12,900 inputs); more: quantisation and the tensor-core tiles, two launches.
+ * Asynchronous, no allocation, capturable.  Device-side failures (a
  * bounded wait that gave up) are reported by ling_moe_fp8_linear_status.
  * Errors: INVALID_ARG (before anything is enqueued), CUDA. */
 int ling_moe_fp8_linear_forward(ling_moe_fp8_linear_t *h, const void *x, int64_t x_stride, int T, void *out,
@@ -470,9 +471,9 @@ typedef struct {
 
 typedef struct ling_moe_delta ling_moe_delta_t; /* opaque handle: the prefill's workspace */
 
-/* Checks cfg and allocates the workspace on the current device (at most about
- * 640 records of 107 KB, one per 64 tokens and head, or one record per head where there
- * are more heads).  Synchronises the device.  As with every handle, one must
+/* Checks cfg and allocates the workspace on the current device: a record of up
+ * to 123 KB per 64 tokens and head of a prefill, at most 16 per SM (292 MB with
+ * 128 x 128 states; one segment of chunks at least).  Synchronises the device.  As with every handle, one must
  * not be used by two streams (or two captured graphs that run at the same
  * time), and its calls belong to its device.
  * Errors: INVALID_ARG, UNSUPPORTED, OOM, CUDA; *out is then NULL. */
@@ -494,7 +495,9 @@ int ling_moe_delta_step(ling_moe_delta_t *h, const ling_moe_delta_io_t *io, int 
  * state stays as it is) and rows behind the last one are left as they were.
  * fresh: uint8 [seqs] (DEVICE) or NULL: sequences that start from a zero state
  * whatever their slot holds.  Chunks of 64 tokens; two launches per segment of
- * chunks that the workspace holds.  Asynchronous, no allocation, capturable.
+ * chunks that half the workspace holds, the second segment's preparation beside
+ * the first one's scan (programmatic launches).  Asynchronous, no allocation,
+ * capturable.
  * Device-side failures (a bounded wait that gave up) are reported by
  * ling_moe_delta_status.  Errors: INVALID_ARG (before anything is enqueued), CUDA. */
 int ling_moe_delta_prefill(ling_moe_delta_t *h, const ling_moe_delta_io_t *io, int tokens, const int32_t *cu_seqlens,

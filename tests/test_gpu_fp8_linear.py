@@ -208,3 +208,26 @@ def test_token_codes_at_the_borders_between_codes(T):
         # one product of a code with the scale, rounded once; below 2^-126 it may flush
         assert (np.abs(y.double().cpu().numpy() - want) <= U * np.abs(want) + 2.0**-126).all()
     f.close()
+
+
+@pytest.mark.parametrize("T,N,K", [(3900, 4100, 300), (4000, 4096, 1024), (3841, 3970, 129)])
+def test_wide_tiles(T, N, K):
+    """Sizes whose tiles are 256 outputs wide, in several waves; the last ones partly empty."""
+    codes, scales = weights(N, K, T)
+    f = lm.BlockFP8Linear(codes, scales, max_tokens=T)
+    x = tokens(T, K, 1)
+    rows = np.unique(np.concatenate([np.linspace(0, T - 1, 30).astype(int), np.arange(T - 70, T, 3)]))
+    for dt in (torch.float32, torch.bfloat16):
+        ob = torch.full((T + 1, N), 7.0, dtype=dt, device=DEV)
+        f.forward(x, out=ob[:T])
+        assert f.status() == lm.LING_MOE_OK
+        check(ob[:T], x, codes, scales, rows)
+        assert (ob[T] == 7).all() and torch.equal(f.forward(x, out_dtype=dt), ob[:T])
+    y = f.forward(x)
+    for cta in (0, 1, 5):  # this CTA loads nothing: its waits run out after 2 ms
+        f.test_set_wait(cta, 2_000_000)
+        f.forward(x)
+        assert f.status() == lm.LING_MOE_ERR_DEVICE_TIMEOUT
+    f.test_set_wait(-1)
+    assert torch.equal(f.forward(x), y) and f.status() == lm.LING_MOE_OK
+    f.close()

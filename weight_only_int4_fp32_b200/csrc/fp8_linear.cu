@@ -294,13 +294,16 @@ __global__ void __launch_bounds__(kGemvWarps * 32, 2) f8_gemv_kernel(const F8Par
 }
 
 // ---------------------------------------------------------------- tensor-core tiles
+constexpr int kF8Scales = 16;
 template <int BN>
 struct F8Cfg {
   static constexpr int kStageA = kF8TileM * kF8Block;  // 16 KB
   static constexpr int kStageB = BN * kF8Block;
   static constexpr int kStages = BN >= 256 ? 4 : BN >= 128 ? 6 : 8;
-  static constexpr int kBarOff = kStages * (kStageA + kStageB);
+  static constexpr int kScaleOff = kStages * (kStageA + kStageB);  // the tokens' scales of kF8Scales blocks
+  static constexpr int kBarOff = kScaleOff + kF8Scales * kF8TileM * 4;
   static constexpr int kSmem = 1024 + kBarOff + 256;
+  static_assert(kStages + 3 <= kF8Scales, "a block's scales are read after its stage may be filled again");
   static constexpr int kTmemCols = 2 * BN;
 };
 constexpr int kF8EpiWarps = 16;
@@ -310,9 +313,92 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t tmem, uint64_t a, uint64_t b,
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, {%5, %6, %7, %8}, p;\n\t}"
-      :: "r"(tmem), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(0), "r"(0), "r"(0), "r"(0));
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, {%5, %5, %5, %5}, p;\n\t}"
+      :: "r"(tmem), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(0));
 }
+// true in one lane of a whole warp, always the same
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+template <typename E>
+__device__ __forceinline__ E to_out(float x) {
+  if constexpr (sizeof(E) == 2)
+    return __float2bfloat16_rn(x);
+  else
+    return x;
+}
+// P lanes with P pieces of 16 bytes each: lane i gets every lane's piece i
+template <int P>
+__device__ __forceinline__ void exchange(uint4 v[P]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = P / 2; o > 0; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      if (i & o) continue;
+      const uint4 x = up ? v[i] : v[i | o];
+      const uint4 y = make_uint4(__shfl_xor_sync(0xffffffffu, x.x, o), __shfl_xor_sync(0xffffffffu, x.y, o),
+                                 __shfl_xor_sync(0xffffffffu, x.z, o), __shfl_xor_sync(0xffffffffu, x.w, o));
+      if (up)
+        v[i] = y;
+      else
+        v[i | o] = y;
+    }
+  }
+}
+// A warp's 32 rows x COLS accumulators (a row per lane) to rows row0 .., columns n0 ..
+// of the output.  Lanes exchange pieces first, so that a store writes whole lines
+// of a few rows: a row per lane, a 256 x 256 tile's stores took 3.6 us.
+template <typename E, int COLS>
+__device__ __forceinline__ void store_tile(const F8Params& p, const float* acc, int row0, int n0) {
+  constexpr int PE = 16 / sizeof(E), ALL = COLS / PE, P = ALL < 8 ? ALL : 8;  // elements of a piece, pieces of a row
+  const int lane = threadIdx.x & 31;
+  E* out = static_cast<E*>(p.out);
+  if (!p.vec) {
+    if (row0 + lane < p.T) {
+#pragma unroll
+      for (int j = 0; j < COLS; ++j)
+        if (n0 + j < p.N) out[(size_t)(row0 + lane) * p.out_stride + n0 + j] = to_out<E>(acc[j]);
+    }
+    return;
+  }
+#pragma unroll
+  for (int g = 0; g < ALL; g += P) {
+    uint4 v[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const float* x = acc + (g + i) * PE;
+      if constexpr (sizeof(E) == 2) {
+        __nv_bfloat162 r[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[e] = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+        v[i] = *reinterpret_cast<const uint4*>(r);
+      } else {
+        v[i] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+      }
+    }
+    exchange<P>(v);
+    const int n = n0 + (g + (lane & (P - 1))) * PE;
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+      const int row = row0 + (lane & ~(P - 1)) + j;
+      if (row >= p.T) continue;
+      E* dst = out + (size_t)row * p.out_stride + n;
+      if (n + PE <= p.N) {
+        *reinterpret_cast<uint4*>(dst) = v[j];
+      } else {
+        const E* e = reinterpret_cast<const E*>(&v[j]);
+#pragma unroll
+        for (int i = 0; i < PE; ++i)
+          if (n + i < p.N) dst[i] = e[i];
+      }
+    }
+  }
+}
+
 // N consecutive columns of this warp's 32 TMEM lanes, here when it returns
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, float* v) {
@@ -362,6 +448,10 @@ __device__ __forceinline__ void tile_place(const F8Params& p, int tile, int& m, 
 // Warps 0-15 promote and store (TMEM lanes 32 (w % 4).., column quarter w / 4),
 // warp 16 issues the TMA loads, warp 17 the MMAs.  Every role walks the tiles
 // blockIdx.x, + gridDim.x, ...
+// (256 x 256 tiles over the two CTAs of a cluster, which read a third less, were
+// slower: 396 us in place of 375 for 8192 x 8192 x 4096.  A buffer's way from the
+// MMAs to the promotion and back takes longer between two CTAs, and it is what
+// bounds the loop.)
 template <int BN>
 __global__ void __launch_bounds__(kF8Threads, 1)
 f8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const F8Params p) {
@@ -372,6 +462,7 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw_f8) + 1023) & ~uintptr_t(1023));
   unsigned char* sA = smem;
   unsigned char* sB = smem + S * C::kStageA;
+  float* sX = reinterpret_cast<float*>(smem + C::kScaleOff);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
   uint64_t* empty = full + S;
   uint64_t* accf = empty + S;
@@ -417,25 +508,24 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
       int tm, tn;
       tile_place(p, tile, tm, tn);
       const int m0 = tm * kF8TileM, n0 = tn * BN + part * COLS;
-      const int row = m0 + 32 * q + lane;
-      const float* sx = p.sx + row;  // rows up to tpad exist
+      // the weights' scales of 32 blocks, one per lane, loaded 32 blocks ahead
       const float* sw = p.sw + (size_t)min(n0 / kF8Block, (p.N - 1) / kF8Block) * p.kb;
       float acc[COLS];
 #pragma unroll
       for (int j = 0; j < COLS; ++j) acc[j] = 0.f;
-      float sx_next = __ldcg(sx), sw_next = __ldg(sw);  // a block ahead, multiplied when it is their turn
+      float sw_now = 0.f, sw_next = lane < p.kb ? __ldg(sw + lane) : 0.f;
 #pragma unroll 1
       for (int kb = 0; kb < p.kb; ++kb, ++it) {
         const int b = it & 1;
-        const float s = sx_next * sw_next;
-        if (kb + 1 < p.kb) {
-          sx_next = __ldcg(sx + (size_t)(kb + 1) * p.tpad);
-          sw_next = __ldg(sw + kb + 1);
+        if ((kb & 31) == 0) {
+          sw_now = sw_next;
+          if (kb + 32 + lane < p.kb) sw_next = __ldg(sw + kb + 32 + lane);
         }
         if (lane == 0) ok = tc_wait(&accf[b], (it >> 1) & 1, p.err, abort_flag, p.wait_ns);
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
         tc_fence_after();
+        const float s = sX[(it % kF8Scales) * kF8TileM + 32 * q + lane] * __shfl_sync(0xffffffffu, sw_now, kb & 31);
 #pragma unroll
         for (int c = 0; c < COLS; c += CH) {
           float v[CH];
@@ -450,89 +540,68 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
         }
       }
       if (!ok) break;
-      if (row < p.T) {
-        const size_t at = (size_t)row * p.out_stride + n0;
-        if (p.out_bf16) {
-          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + at;
-#pragma unroll
-          for (int j = 0; j < COLS; j += 8) {
-            if (p.vec && n0 + j + 8 <= p.N) {
-              __nv_bfloat162 r[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) r[i] = __floats2bfloat162_rn(acc[j + 2 * i], acc[j + 2 * i + 1]);
-              *reinterpret_cast<uint4*>(o + j) = *reinterpret_cast<const uint4*>(r);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (n0 + j + i < p.N) o[j + i] = __float2bfloat16_rn(acc[j + i]);
-            }
-          }
-        } else {
-          float* o = static_cast<float*>(p.out) + at;
-#pragma unroll
-          for (int j = 0; j < COLS; j += 4) {
-            if (p.vec && n0 + j + 4 <= p.N) {
-              *reinterpret_cast<float4*>(o + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (n0 + j + i < p.N) o[j + i] = acc[j + i];
-            }
-          }
-        }
-      }
+      if (p.out_bf16)
+        store_tile<__nv_bfloat16, COLS>(p, acc, m0 + 32 * q, n0);
+      else
+        store_tile<float, COLS>(p, acc, m0 + 32 * q, n0);
     }
   } else if (warp == kF8EpiWarps) {
-    if (lane == 0) {
-      int g = 0;
-      bool ok = (int)blockIdx.x != p.skip_cta;
-      for (int tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x) {
-        int tm, tn;
-        tile_place(p, tile, tm, tn);
-        const int m0 = tm * kF8TileM, n0 = tn * BN;
+    // (here and below the whole warp walks the loop and one lane issues, so that
+    // addresses and descriptors stay in uniform registers)
+    int g = 0;
+    bool ok = (int)blockIdx.x != p.skip_cta;
+    for (int tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x) {
+      int tm, tn;
+      tile_place(p, tile, tm, tn);
+      const int m0 = tm * kF8TileM, n0 = tn * BN;
+      const float* sx = p.sx + m0;  // rows up to tpad exist
 #pragma unroll 1
-        for (int kb = 0; kb < p.kb; ++kb, ++g) {
-          const int s = g % S;
-          if (!tc_wait(&empty[s], ((g / S) & 1) ^ 1, p.err, abort_flag, p.wait_ns)) {
-            ok = false;
-            break;
-          }
-          mbar_arrive_expect_tx(&full[s], C::kStageA + C::kStageB);
+      for (int kb = 0; kb < p.kb; ++kb, ++g) {
+        const int s = g % S;
+        ok = __all_sync(0xffffffffu, tc_wait(&empty[s], ((g / S) & 1) ^ 1, p.err, abort_flag, p.wait_ns));
+        if (!ok) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&full[s], C::kStageA + C::kStageB + kF8TileM * 4);
+          bulk_g2s(sX + (g % kF8Scales) * kF8TileM, sx + (size_t)kb * p.tpad, kF8TileM * 4, &full[s]);
           tma_load_2d(smem_u32(sA + s * C::kStageA), &tmX, kb * kF8Block, m0, &full[s]);
           tma_load_2d(smem_u32(sB + s * C::kStageB), &tmW, kb * kF8Block, n0, &full[s]);
         }
+        __syncwarp();
       }
-      // after an abort, loads may still be landing: wait for every armed stage
-      for (int i = g > S ? g - S : 0; i < g; ++i) mbar_wait(&full[i % S], (i / S) & 1, kTcWaitNs, p.err);
     }
+    // after an abort, loads may still be landing: wait for every armed stage
+    for (int i = g > S ? g - S : 0; i < g; ++i) mbar_wait(&full[i % S], (i / S) & 1, kTcWaitNs, p.err);
     __syncwarp();
   } else {
-    if (lane == 0) {
-      const uint32_t idesc = make_idesc(BN);  // f32 accumulator; e4m3 is format 0, as f16 is in kind::f16
-      int g = 0;
-      bool ok = true;
-      for (int tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x) {
+    // f32 accumulator; e4m3 is format 0, as f16 is in kind::f16
+    const uint32_t idesc = make_idesc(BN);
+    const uint64_t da = sw128_desc(smem_u32(sA)), db = sw128_desc(smem_u32(sB));
+    int g = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x) {
 #pragma unroll 1
-        for (int kb = 0; kb < p.kb; ++kb, ++g) {
-          const int s = g % S, b = g & 1;
-          if (!tc_wait(&full[s], (g / S) & 1, p.err, abort_flag, p.wait_ns) ||
-              !tc_wait(&acce[b], ((g >> 1) & 1) ^ 1, p.err, abort_flag, p.wait_ns)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t a0 = smem_u32(sA + s * C::kStageA), b0 = smem_u32(sB + s * C::kStageB);
+      for (int kb = 0; kb < p.kb; ++kb, ++g) {
+        const int s = g % S, b = g & 1;
+        ok = __all_sync(0xffffffffu, tc_wait(&full[s], (g / S) & 1, p.err, abort_flag, p.wait_ns) &&
+                                         tc_wait(&acce[b], ((g >> 1) & 1) ^ 1, p.err, abort_flag, p.wait_ns));
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          // descriptors count 16 bytes
+          const uint64_t a0 = da + (uint64_t)(s * (C::kStageA >> 4)), b0 = db + (uint64_t)(s * (C::kStageB >> 4));
 #pragma unroll
           for (int k4 = 0; k4 < kF8Block / 32; ++k4)
-            tc_mma_f8(tmem + b * BN, sw128_desc(a0 + 32 * k4), sw128_desc(b0 + 32 * k4), idesc, k4 ? 1u : 0u);
+            tc_mma_f8(tmem + b * BN, a0 + 2 * k4, b0 + 2 * k4, idesc, k4 ? 1u : 0u);
           tc_commit(&empty[s]);
           tc_commit(&accf[b]);
         }
+        __syncwarp();
       }
-      // no MMA may still be writing TMEM when it is freed
-      tc_commit(drain);
-      mbar_wait(drain, 0, kTcWaitNs, p.err);
     }
+    // no MMA may still be writing TMEM when it is freed (the lane that issued them commits)
+    if (elect_one()) tc_commit(drain);
+    __syncwarp();
+    mbar_wait(drain, 0, kTcWaitNs, p.err);
     __syncwarp();
   }
   tc_fence_before();
@@ -609,12 +678,16 @@ cudaError_t launch_f8_gemv(const F8Params& p, int sms, bool fused, cudaStream_t 
   return cudaLaunchKernelEx(&c, f8_gemv_kernel<true>, p);
 }
 
+template <int BN>
+static cudaError_t gemm_launch(const F8Maps& m, const F8Params& p, int tile, int ctas, cudaStream_t s) {
+  return launch_dependent(f8_gemm_kernel<BN>, ctas, kF8Threads, F8Cfg<BN>::kSmem, s, m.x, m.w[tile], p);
+}
 cudaError_t launch_f8_gemm(const F8Maps& m, const F8Params& p, int tile, int ctas, cudaStream_t s) {
   switch (tile) {
-    case 0: return launch_dependent(f8_gemm_kernel<32>, ctas, kF8Threads, F8Cfg<32>::kSmem, s, m.x, m.w[0], p);
-    case 1: return launch_dependent(f8_gemm_kernel<64>, ctas, kF8Threads, F8Cfg<64>::kSmem, s, m.x, m.w[1], p);
-    case 2: return launch_dependent(f8_gemm_kernel<128>, ctas, kF8Threads, F8Cfg<128>::kSmem, s, m.x, m.w[2], p);
-    default: return launch_dependent(f8_gemm_kernel<256>, ctas, kF8Threads, F8Cfg<256>::kSmem, s, m.x, m.w[3], p);
+    case 0: return gemm_launch<32>(m, p, tile, ctas, s);
+    case 1: return gemm_launch<64>(m, p, tile, ctas, s);
+    case 2: return gemm_launch<128>(m, p, tile, ctas, s);
+    default: return gemm_launch<256>(m, p, tile, ctas, s);
   }
 }
 
