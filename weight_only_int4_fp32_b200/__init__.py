@@ -673,8 +673,6 @@ class BlockFP8Linear(_Handle):
         _require(codes, tuple(codes.shape), codes.dtype, True, "codes")
         _require(scales, (-(-codes.shape[0] // 128), -(-codes.shape[1] // 128)), torch.float32, True, "scales")
         _on_current_device(torch, "BlockFP8Linear", codes, scales)
-        # the library copies on the legacy default stream: what the caller's stream still writes has to be there
-        torch.cuda.current_stream().synchronize()
         h = ctypes.c_void_p()
         _check(lib.ling_moe_fp8_linear_create(codes.data_ptr(), scales.data_ptr(), self.out_features,
                                               self.in_features, self.max_tokens, ctypes.byref(h)))

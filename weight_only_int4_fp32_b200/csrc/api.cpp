@@ -238,8 +238,11 @@ static int create_impl(const ling_moe_config_t* cfg, const ling_moe_weights_t* w
     }
   }
 
+  // The weights may still be on their way on any of the caller's streams, which
+  // the stream below does not follow.
   cudaStream_t s = nullptr;
-  e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
+  e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
   if (e == cudaSuccess) e = cudaMemcpyAsync(h->router_w, w->router_w, (size_t)E * kH * bf, cudaMemcpyDeviceToDevice, s);
   if (e == cudaSuccess && w->router_bias)
     e = cudaMemcpyAsync(h->router_bias, w->router_bias, (size_t)E * sizeof(float), cudaMemcpyDeviceToDevice, s);
@@ -628,7 +631,8 @@ int ling_moe_lmhead_create(const void* w, int vocab, int hidden, ling_moe_lmhead
       return rc;
     }
   }
-  e = cudaMemset(h->err, 0, sizeof(unsigned int));
+  e = cudaDeviceSynchronize();  // w may still be on its way on another stream
+  if (e == cudaSuccess) e = cudaMemset(h->err, 0, sizeof(unsigned int));
   if (e == cudaSuccess)
     e = launch_lmh_quantize(static_cast<const __nv_bfloat16*>(w), vocab, hidden, h->codes, h->scales, nullptr);
   if (e == cudaSuccess) e = cudaDeviceSynchronize();

@@ -59,6 +59,7 @@ int ling_moe_fp8_linear_create(const uint8_t* codes, const float* scales, int ou
   const int wrows = (out_features + kF8Block - 1) / kF8Block * kF8Block;
   const size_t nsw = (size_t)(wrows / kF8Block) * h->kb * sizeof(float);
   const size_t nsx = (size_t)h->kb * h->tpad * sizeof(float);
+  e = cudaDeviceSynchronize();  // the weights may still be on their way on any of the caller's streams
   struct { void** p; size_t n; } plan[] = {{(void**)&h->w, (size_t)wrows * pitch},
                                            {(void**)&h->sw, nsw},
                                            {(void**)&h->xq, (size_t)h->tpad * pitch},
