@@ -218,3 +218,21 @@ def test_reorder_many_tensors_and_refusals():
     bs.reorder([], parents)
     bs.reorder([torch.zeros(G * W, 0, device=DEV)], parents)
     bs.close()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_select_more_equal_logits_than_the_candidates_fit(dtype):
+    """600 rows in one piece each, the largest logit of a row on the tokens of 30 of a CTA's 256 threads: few enough
+    threads to be looked at once more, but more candidates than their buffer takes."""
+    G, W, V = 100, 6, 40000
+    bs = lm.BeamSearch(G, W, V)
+    z, c = make(G, W, V, dtype, 21, scale=0.5)
+    z.clamp_(max=5.0)
+    vec = 8 if dtype == torch.bfloat16 else 4
+    t = torch.arange(V, device=DEV)
+    own = (t % (256 * vec)) // vec
+    z[:, :, own < 30] = 7.0
+    z[::2, 3] = z[::2, 2]      # equal rows
+    z[1::3, :, 5] = 8.0        # one above them
+    check(bs, z, c)
+    bs.close()

@@ -26,8 +26,9 @@
 // sums and merges their sorted lists (a lane per segment), then one warp merges
 // the rows (a lane per row).
 //
-// Bound: HBM for large batches, latency (one tile, two merges) for one
-// request.  The segments depend on the call's sizes alone, not on
+// Bound: issue slots of max and exp for large batches (224 live rows x 157184
+// bf16: 30 us, 70 MB at 2.3 TB/s; 55 us with candidates collected tile by tile),
+// latency (one or two tiles, two merges) for one request (9 us).  The segments depend on the call's sizes alone, not on
 // alignment, so equal rows give equal sums to the last bit.
 #include "beam.h"
 #include "common.cuh"
@@ -506,7 +507,7 @@ cudaError_t launch_beam_select(const BeamSelectParams& p, bool bf16, cudaStream_
 // row that is both read and overwritten (a chain or a cycle of parents) needs
 // no copy elsewhere.  Places whose parent is themselves are neither read nor
 // written.  Bound: HBM, moved rows read (shared parents once, the repeats hit
-// the caches) and written once.
+// the caches) and written once: 48 rows of 2 MB moved in 32 us, 6.3 TB/s.
 template <typename U, int MAXW>
 __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const BeamReorderParams p) {
   const int g = blockIdx.y, t = blockIdx.z;

@@ -72,16 +72,22 @@ __device__ __forceinline__ float warp_max_abs(float m) {
 }
 __device__ __forceinline__ int clamp_int(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
 
-// One warp: the sequence and place of chunk `chunk` (counted over all
-// sequences in order), or false.  Boundaries outside [0, T] or out of order
-// are clamped.
-__device__ bool find_chunk(const DeltaParams& p, int chunk, int& seq, int& start, int& len) {
+// the sequence's row of the state pool, -1 for none
+__device__ __forceinline__ int slot_of(const DeltaParams& p, int seq) {
+  const int s = p.slots ? p.slots[seq] : seq;
+  return s >= 0 && s < p.num_slots ? s : -1;
+}
+// One warp: the place of chunk `chunk` (counted over all sequences in order) and
+// its sequence's slot, or false.  Boundaries outside [0, T] or out of order are
+// clamped.
+__device__ bool find_chunk(const DeltaParams& p, int chunk, int& slot, int& start, int& len) {
   const int lane = threadIdx.x & 31;
   int base = 0;
   for (int i0 = 0; i0 < p.nseq; i0 += 32) {
     const int i = i0 + lane;
-    int s = 0, e = 0;
+    int s = 0, e = 0, sl = -1;
     if (i < p.nseq) {
+      sl = slot_of(p, i);
       s = clamp_int(p.cu[i], 0, p.T);
       e = clamp_int(p.cu[i + 1], s, p.T);
     }
@@ -96,7 +102,7 @@ __device__ bool find_chunk(const DeltaParams& p, int chunk, int& seq, int& start
     const unsigned int who = __ballot_sync(0xffffffffu, at >= 0 && at < n);
     if (who) {
       const int l = __ffs(who) - 1;
-      seq = i0 + l;
+      slot = __shfl_sync(0xffffffffu, sl, l);
       start = __shfl_sync(0xffffffffu, s + at * kDeltaChunk, l);
       len = min(kDeltaChunk, __shfl_sync(0xffffffffu, e, l) - start);
       return true;
@@ -117,12 +123,6 @@ __device__ void find_sequence(const DeltaParams& p, int seq, int& first, int& st
   start = clamp_int(p.cu[seq], 0, p.T);
   end = clamp_int(p.cu[seq + 1], start, p.T);
 }
-// the sequence's row of the state pool, -1 for none
-__device__ __forceinline__ int slot_of(const DeltaParams& p, int seq) {
-  const int s = p.slots ? p.slots[seq] : seq;
-  return s >= 0 && s < p.num_slots ? s : -1;
-}
-
 // N consecutive channels of a bf16 row, two to a word; converted apart from the
 // load, so that a thread's loads are in flight together
 template <int N>
@@ -215,6 +215,10 @@ __device__ __forceinline__ float transpose_sum32(float v[32]) {
 // S^T q + (k . q) u.  The warps of a CTA share the tokens' unit keys and
 // queries and their decays, which a warp per token prepares while the state is
 // on its way from HBM.
+// HBM bound for many heads: 64 sequences x 4 tokens, 32 heads of 128 x 128, 65 us,
+// 268 MB of states at 4.1 TB/s (32 columns per CTA with an exchange between its
+// warps per token: 89 us; without packed arithmetic and the next head's state on
+// its way: 86).  One sequence, one token: 4.3 us on the device.
 constexpr int kStepCols = 16;  // state columns of a warp
 // the place of channel c among a token's channels: R of them per row group, padded so
 // that the eight row groups' 16-byte reads fall into different banks
@@ -449,6 +453,10 @@ __global__ void __launch_bounds__(256, 2) delta_step_kernel(const DeltaParams p)
 // exp(G_last) fp32 [dk] | U~^T fp32 in the order of the accumulators that take it.
 // fp16 rows have their 16-byte
 // pieces exchanged, piece ^= row % 8, for conflict-free ldmatrix.
+//
+// 56 us for 576 records of 128 x 128 heads (81 KB read, 123 KB written each): two
+// CTAs per SM (shared memory, 128 registers), whose own loads and dependent
+// phases are what the time goes to, not a rate.
 template <int DK>
 struct PrepCfg {
   static constexpr int kFRow = DK + 8;            // floats of a row of k p or k s
@@ -509,8 +517,8 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
   const int h = blockIdx.x % p.Hv, hk = h / (p.Hv / p.Hk);
   pdl_launch_dependents();
   if (warp == 0) {
-    int seq = 0, start = 0, len = 0;
-    const bool ok = find_chunk(p, p.seg0 + (int)(blockIdx.x / p.Hv), seq, start, len) && slot_of(p, seq) >= 0;
+    int slot = -1, start = 0, len = 0;
+    const bool ok = find_chunk(p, p.seg0 + (int)(blockIdx.x / p.Hv), slot, start, len) && slot >= 0;
     if (lane == 0) {
       info[0] = ok ? len : 0;
       info[1] = start;
@@ -527,6 +535,10 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
     return;
   }
   unsigned char* rec = p.ws + (size_t)blockIdx.x * delta_rec_bytes(DK, p.dv);
+  if (tid < len) {  // v is used last: to L2 by then
+    const char* row = reinterpret_cast<const char*>(p.v + (long long)(start + tid) * p.v_t + h * p.v_h);
+    for (int i = 0; i < 2 * p.dv; i += 128) asm volatile("prefetch.global.L2 [%0];" :: "l"(row + i));
+  }
 
   // ---- this warp's 8 rows, CPL channels per lane
   const int row0 = 8 * warp, c0 = CPL * lane;
@@ -977,8 +989,9 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
 // operands through shared memory, with a barrier of the two each.  Operands are
 // two fp16 terms, a power of two per state column and half.  One more warp
 // brings the records, two ahead, by bulk copies.
-// The tensor cores' fp16 rate bounds it where there are sequences and heads
-// enough, the chain of mma.sync and exchanges of one chunk where there are few.
+// A chunk takes 4200 cycles, 1.9 k of them mma.sync issue on each of the four
+// schedulers (18 chunks x 32 heads: 45 us); with a barrier of the whole CTA after
+// each of three products, and the inverse applied here, it took 7500.
 constexpr int kScanTiles = 2;  // 16-column tiles per CTA
 
 template <int DK>
@@ -1282,7 +1295,9 @@ static void step_launch(const DeltaParams& p, unsigned grid, int warps, cudaStre
 cudaError_t launch_delta_step(const DeltaParams& p, int dk, int sms, cudaStream_t s) {
   const long long heads = (long long)p.nseq * p.Hv;
   int warps = p.dv / kStepCols;
-  const int fit = sms * 16 / warps;  // 16 warps per SM (registers)
+  // what an SM holds: 16 warps (registers), 227 KB of shared memory
+  const int smem = (dk == 64 ? step_smem<64>(p.dv, true) : step_smem<128>(p.dv, true)) + 1024;
+  const int fit = sms * (16 / warps < 227 * 1024 / smem ? 16 / warps : 227 * 1024 / smem);
   if (heads > fit) {
     if (dk == 64)
       step_launch<64, true>(p, (unsigned)fit, warps, s);
