@@ -16,7 +16,8 @@
 //    fragments (e4m3 -> fp16 exactly), 16 outputs at a time per CTA, the blocks
 //    of K dealt to its 8 warps, tokens quantised in the same launch.  Bound:
 //    HBM, N x K bytes; at sizes of one projection, latency (2560 x 2560, one
-//    token: 5.5 us on the device; 8192 x 2560, eight: 13 us).
+//    token: 5.5 us on the device; 8192 x 2560, eight: 11.4 us, 8 of them without
+//    the quantisation).
 //  * more: tcgen05 (kind::f8f6f4) tiles of 128 tokens x 32..256 outputs.  Each
 //    128-wide K block is one pipeline stage and one chain of four MMAs into
 //    one of two TMEM buffers; 16 warps read a finished buffer, scale it and
@@ -134,7 +135,7 @@ __global__ void __launch_bounds__(256) f8_quantize_kernel(const __nv_bfloat16* _
 // rows g and g + 8; the K order inside the MMAs is a permutation of the 64
 // codes, the same for weights and tokens.
 //
-// The CTAs of a cluster (one, or four where there is much to do) quantise the
+// The CTAs of a cluster (one, or two where there is much to do) quantise the
 // tokens into the shared memory of each while their first weights are on their
 // way: one launch.  Where the tokens' codes do not fit there (FUSED false), the
 // kernel above has left them in global memory.
@@ -179,46 +180,58 @@ __global__ void __launch_bounds__(kGemvWarps * 32, 2) f8_gemv_kernel(const F8Par
       b[u][h] = ldg_stream(wa + 8 * pitch + 64 * h);
     }
   };
-#pragma unroll
-  for (int u = 0; u < kU; ++u) load(u, blockIdx.x, warp + kGemvWarps * u);
-
   // the tokens: row pitch in bytes (half a bank row off a multiple of 128), scales [kb][T]
   const int row = (int)pitch + 64;
   float* ssx = reinterpret_cast<float*>(gsm + (size_t)p.T * row);
   const int tg = min(g, p.T - 1), t0 = min(2 * c, p.T - 1), t1 = min(2 * c + 1, p.T - 1);  // past T: results dropped
-  if constexpr (FUSED) {
-    const int l = threadIdx.x & 15, pairs = p.T * p.kb;
-    const int ctas = (int)cluster_ctas(), step = 16 * ctas;
-    constexpr int kQ = 4;
-    int i = (threadIdx.x >> 4) + 16 * (int)cluster_rank(), t = i / p.kb, kb = i - t * p.kb;  // token and block of a pair
-    const int dt = step / p.kb, dkb = step - dt * p.kb;
-    cluster_wait();  // every CTA of the cluster runs
-    while (i < pairs) {
-      uint32_t r[kQ][4];
-      int at[kQ], as[kQ];
+  // quantisation: kQ pairs of token and block at a time per 16 lanes
+  constexpr int kQ = 3;
+  const int l = threadIdx.x & 15, pairs = FUSED ? p.T * p.kb : 0;
+  const int ctas = FUSED ? (int)cluster_ctas() : 1, step = 16 * ctas;
+  int qi = (threadIdx.x >> 4) + (FUSED ? 16 * (int)cluster_rank() : 0), qt = qi / p.kb, qb = qi - qt * p.kb;
+  const int dt = step / p.kb, db = step - dt * p.kb;
+  uint32_t qr[kQ][4];
+  int at[kQ], as[kQ];
+  auto fetch = [&] {
 #pragma unroll
-      for (int q = 0; q < kQ; ++q) {
-        at[q] = -1;
-        if (i < pairs) {
-          load8(p.x + t * p.x_stride + kb * kF8Block + 8 * l, kb * kF8Block + 8 * l, p.K, p.x_vec, r[q]);
-          at[q] = t * row + kb * kF8Block + 8 * l;
-          as[q] = p.T * row + 4 * (kb * p.T + t);
-        }
-        i += step, t += dt, kb += dkb;
-        if (kb >= p.kb) kb -= p.kb, ++t;
+    for (int q = 0; q < kQ; ++q) {
+      at[q] = -1;
+      qr[q][0] = qr[q][1] = qr[q][2] = qr[q][3] = 0u;
+      if (qi < pairs) {
+        const int k = qb * kF8Block + 8 * l;
+        load8(p.x + qt * p.x_stride + k, k, p.K, p.x_vec, qr[q]);
+        at[q] = qt * row + k;
+        as[q] = p.T * row + 4 * (qb * p.T + qt);
       }
+      qi += step, qt += dt, qb += db;
+      if (qb >= p.kb) qb -= p.kb, ++qt;
+    }
+  };
+  if constexpr (FUSED) fetch();  // before the weights: they would wait behind them
+#pragma unroll
+  for (int u = 0; u < kU; ++u) load(u, blockIdx.x, warp + kGemvWarps * u);
+
+  if constexpr (FUSED) {
+    cluster_wait();  // every CTA of the cluster runs
+    while (true) {
+      float qs[kQ];
+      uint2 codes[kQ];
+#pragma unroll
+      for (int q = 0; q < kQ; ++q) qs[q] = block_scale16(qr[q]);  // side by side: nothing leaves the loop early
+#pragma unroll
+      for (int q = 0; q < kQ; ++q) codes[q] = f8_codes(qr[q], qs[q]);
 #pragma unroll
       for (int q = 0; q < kQ; ++q) {
-        if (at[q] < 0) break;  // whole 16-lane groups
-        const float s = block_scale16(r[q]);
-        const uint2 codes = f8_codes(r[q], s);
+        if (at[q] < 0) continue;
         for (int k = 0; k < ctas; ++k) {
           const uint32_t base = cluster_map(smem_u32(gsm), (uint32_t)k);
-          asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" :: "r"(base + at[q]), "r"(codes.x), "r"(codes.y)
+          asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" :: "r"(base + at[q]), "r"(codes[q].x), "r"(codes[q].y)
                        : "memory");
-          if (l == 0) asm volatile("st.shared::cluster.f32 [%0], %1;" :: "r"(base + as[q]), "f"(s) : "memory");
+          if (l == 0) asm volatile("st.shared::cluster.f32 [%0], %1;" :: "r"(base + as[q]), "f"(qs[q]) : "memory");
         }
       }
+      if (qi >= pairs) break;
+      fetch();
     }
     cluster_arrive();
     cluster_wait();
@@ -664,8 +677,10 @@ cudaError_t launch_f8_gemv(const F8Params& p, int sms, bool fused, cudaStream_t 
   const int groups = (p.N + kGemvRows - 1) / kGemvRows;
   int grid = groups < 2 * sms ? groups : 2 * sms;
   if (!fused) return launch_dependent(f8_gemv_kernel<false>, grid, kGemvWarps * 32, 0, s, p);
-  // a CTA alone quantises 64 blocks of 128 inputs in one round of loads
-  const int cluster = p.T * p.kb > 64 && grid >= 4 ? 4 : 1;
+  // Two CTAs share the quantisation where one alone would take more than a round
+  // or two of loads: 8 tokens x 2560 inputs, 8192 outputs, 11.4 us (alone 14.5, four
+  // 12.2, eight 12.6).
+  const int cluster = p.T * p.kb > 64 && grid >= 2 ? 2 : 1;
   grid = (grid + cluster - 1) / cluster * cluster;
   cudaLaunchConfig_t c{};
   c.gridDim = dim3((unsigned)grid);
