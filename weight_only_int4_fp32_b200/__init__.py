@@ -752,13 +752,17 @@ class GatedDeltaRule(_Handle):
         gc = g.dim() == nl + 2
         dev = torch.cuda.current_device() if q.is_cuda else -2
         bf16, f32 = torch.bfloat16, torch.float32
-        qk = (*lead, Hk, dk)
-        vh, bh = (*lead, Hv, dv), (*lead, Hv)
-        for name, t, shape, dt in (("q", q, qk, bf16), ("k", k, qk, bf16), ("v", v, vh, bf16),
-                                   ("g", g, (*lead, Hv, dk) if gc else bh, f32), ("beta", beta, bh, f32)):
-            if t.shape != shape or t.dtype != dt or t.get_device() != dev:
-                raise ValueError(f"{name} must be a CUDA {dt} tensor of shape {shape} on the current device, got {t.dtype} "
-                                 f"{tuple(t.shape)} on {t.device}")
+        qk, vh, bh = (*lead, Hk, dk), (*lead, Hv, dv), (*lead, Hv)
+        gh = (*lead, Hv, dk) if gc else bh
+        if not (q.shape == qk and k.shape == qk and v.shape == vh and g.shape == gh and beta.shape == bh
+                and q.dtype == bf16 and k.dtype == bf16 and v.dtype == bf16 and g.dtype == f32 and beta.dtype == f32
+                and q.get_device() == dev and k.get_device() == dev and v.get_device() == dev and g.get_device() == dev
+                and beta.get_device() == dev):
+            for name, t, shape, dt in (("q", q, qk, bf16), ("k", k, qk, bf16), ("v", v, vh, bf16), ("g", g, gh, f32),
+                                       ("beta", beta, bh, f32)):
+                if t.shape != shape or t.dtype != dt or t.get_device() != dev:
+                    raise ValueError(f"{name} must be a CUDA {dt} tensor of shape {shape} on the current device, got "
+                                     f"{t.dtype} {tuple(t.shape)} on {t.device}")
         sq, sk, sv, sg, sb = q.stride(), k.stride(), v.stride(), g.stride(), beta.stride()
         if sq[-1] != 1 or sk[-1] != 1 or sv[-1] != 1:
             raise ValueError("q, k and v must be contiguous along their last dimension")
