@@ -490,9 +490,10 @@ int ling_moe_delta_step(ling_moe_delta_t *h, const ling_moe_delta_io_t *io, int 
                         const int32_t *accepted, void *stream);
 
 /* Packed prompts: sequence i is tokens [cu_seqlens[i], cu_seqlens[i + 1]) of the
- * call's [tokens, ...] tensors (int32 [seqs + 1], DEVICE, ascending from 0; values
- * outside [0, tokens] or descending are clamped).  A sequence may be empty (its
- * state stays as it is) and rows behind the last one are left as they were.
+ * call's [tokens, ...] tensors (int32 [seqs + 1], DEVICE, ascending from 0; a value
+ * outside [0, tokens] counts as the nearest inside, one below an earlier one as
+ * that one, so that sequences never overlap).  A sequence may be empty (its state
+ * stays as it is) and rows behind the last one are left as they were.
  * fresh: uint8 [seqs] (DEVICE) or NULL: sequences that start from a zero state
  * whatever their slot holds.  Chunks of 64 tokens; two launches per segment of
  * chunks that half the workspace holds, the second segment's preparation beside

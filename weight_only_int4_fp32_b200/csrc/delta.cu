@@ -77,21 +77,35 @@ __device__ __forceinline__ int slot_of(const DeltaParams& p, int seq) {
   const int s = p.slots ? p.slots[seq] : seq;
   return s >= 0 && s < p.num_slots ? s : -1;
 }
+// One warp, sequence i = a multiple of 32 + lane: its tokens [start, end).  A boundary
+// counts as the largest of those up to it, each clamped to [0, T]: sequences never
+// overlap, so that they have no more chunks than the host made room for.  `run` is the
+// boundary before the 32 sequences, and then the one behind them.
+__device__ __forceinline__ void scan_bounds(const DeltaParams& p, int i, int& run, int& start, int& end) {
+  const int lane = threadIdx.x & 31;
+  end = i < p.nseq ? clamp_int(p.cu[i + 1], 0, p.T) : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, end, o);
+    if (lane >= o) end = max(end, y);
+  }
+  end = max(end, run);
+  start = __shfl_up_sync(0xffffffffu, end, 1);
+  if (lane == 0) start = run;
+  run = __shfl_sync(0xffffffffu, end, 31);
+}
+__device__ __forceinline__ int chunks_of(int tokens) { return (tokens + kDeltaChunk - 1) / kDeltaChunk; }
 // One warp: the place of chunk `chunk` (counted over all sequences in order) and
-// its sequence's slot, or false.  Boundaries outside [0, T] or out of order are
-// clamped.
+// its sequence's slot, or false.
 __device__ bool find_chunk(const DeltaParams& p, int chunk, int& slot, int& start, int& len) {
   const int lane = threadIdx.x & 31;
-  int base = 0;
+  int base = 0, run = clamp_int(p.cu[0], 0, p.T);
   for (int i0 = 0; i0 < p.nseq; i0 += 32) {
     const int i = i0 + lane;
-    int s = 0, e = 0, sl = -1;
-    if (i < p.nseq) {
-      sl = slot_of(p, i);
-      s = clamp_int(p.cu[i], 0, p.T);
-      e = clamp_int(p.cu[i + 1], s, p.T);
-    }
-    const int n = (e - s + kDeltaChunk - 1) / kDeltaChunk;
+    int s, e;
+    scan_bounds(p, i, run, s, e);
+    const int sl = i < p.nseq ? slot_of(p, i) : -1;
+    const int n = chunks_of(e - s);
     int x = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -114,14 +128,18 @@ __device__ bool find_chunk(const DeltaParams& p, int chunk, int& slot, int& star
 // One warp: sequence seq's first chunk, its tokens [start, end).
 __device__ void find_sequence(const DeltaParams& p, int seq, int& first, int& start, int& end) {
   const int lane = threadIdx.x & 31;
-  int n = 0;
-  for (int i = lane; i < seq; i += 32) {
-    const int s = clamp_int(p.cu[i], 0, p.T), e = clamp_int(p.cu[i + 1], s, p.T);
-    n += (e - s + kDeltaChunk - 1) / kDeltaChunk;
+  int n = 0, run = clamp_int(p.cu[0], 0, p.T);
+  for (int i0 = 0;; i0 += 32) {
+    int s, e;
+    scan_bounds(p, i0 + lane, run, s, e);
+    if (i0 + lane < seq) n += chunks_of(e - s);
+    if (seq < i0 + 32) {
+      start = __shfl_sync(0xffffffffu, s, seq - i0);
+      end = __shfl_sync(0xffffffffu, e, seq - i0);
+      break;
+    }
   }
   first = __reduce_add_sync(0xffffffffu, n);
-  start = clamp_int(p.cu[seq], 0, p.T);
-  end = clamp_int(p.cu[seq + 1], start, p.T);
 }
 // N consecutive channels of a bf16 row, two to a word; converted apart from the
 // load, so that a thread's loads are in flight together
@@ -1038,7 +1056,7 @@ __global__ void __launch_bounds__(ScanCfg<DK>::kThreads, 1) delta_scan_kernel(co
   pdl_wait();
   pdl_launch_dependents();
   const int first = info[0], start = info[1], end = info[2], slot = info[3];
-  const int chunks = (end - start + kDeltaChunk - 1) / kDeltaChunk;
+  const int chunks = chunks_of(end - start);
   const int c0 = max(first, p.seg0), c1 = min(first + chunks, p.seg0 + p.seg_chunks);
   if (slot < 0 || c0 >= c1) return;
   const int n = c1 - c0;
