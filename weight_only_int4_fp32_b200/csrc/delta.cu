@@ -35,6 +35,10 @@ namespace {
 
 constexpr float kOpScale = 1024.f;  // k, q, T and B operands are stored times 2^10
 constexpr float kNormEps = 1e-6f;
+// A row whose sum of squares passes fp32 is taken times 2^-40, twice at most: 128 of the largest
+// bf16 numbers, 2^88 and then 2^48, and the sum stays above 2^48, beside which the 1e-6 is nothing.
+constexpr float kNormDown = 0x1p-40f;
+constexpr int kNormPasses = 2;
 constexpr unsigned long long kLandNs = 2000000000ull;
 
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -273,10 +277,19 @@ struct StepRaw {
     float q[CPL], k[CPL];
     from_bf16<CPL>(rq, q);
     from_bf16<CPL>(rk, k);
-    float qq = 0.f, kk = 0.f, kq = 0.f;
+    float qq, kk, kq = 0.f;
+#pragma unroll 1
+    for (int pass = 0;; ++pass) {
+      qq = kk = 0.f;
 #pragma unroll
-    for (int c = 0; c < CPL; ++c) qq += q[c] * q[c], kk += k[c] * k[c];
-    const float rq = 1.f / sqrtf(warp_sum(qq) + kNormEps), rk = 1.f / sqrtf(warp_sum(kk) + kNormEps);
+      for (int c = 0; c < CPL; ++c) qq += q[c] * q[c], kk += k[c] * k[c];
+      qq = warp_sum(qq), kk = warp_sum(kk);
+      if (pass == kNormPasses || !(qq == INFINITY || kk == INFINITY)) break;
+      const float dq = qq == INFINITY ? kNormDown : 1.f, dk = kk == INFINITY ? kNormDown : 1.f;
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) q[c] *= dq, k[c] *= dk;
+    }
+    const float rq = 1.f / sqrtf(qq + kNormEps), rk = 1.f / sqrtf(kk + kNormEps);
 #pragma unroll
     for (int c = 0; c < CPL; ++c) {
       const int at = step_at<DK>(CPL * lane + c);
@@ -587,24 +600,37 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
     sbeta[r] = r < len ? p.beta[(long long)(start + r) * p.be_t + h * p.be_h] : 0.f;
   }
   {
-    float n[16];
+    // lanes 2 i and 2 i + 1: the sum of squares of query i, lanes 16 + 2 i and 17 + 2 i of key i
+    float sum;
+#pragma unroll 1
+    for (int pass = 0;; ++pass) {
+      float n[16];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      n[i] = n[8 + i] = 0.f;
+      for (int i = 0; i < 8; ++i) {
+        n[i] = n[8 + i] = 0.f;
 #pragma unroll
-      for (int c = 0; c < CPL; ++c) n[i] = fmaf(q[i][c], q[i][c], n[i]), n[8 + i] = fmaf(k[i][c], k[i][c], n[8 + i]);
-    }
-    // lanes 2 i and 2 i + 1 are left with the sum of n[i]
+        for (int c = 0; c < CPL; ++c) n[i] = fmaf(q[i][c], q[i][c], n[i]), n[8 + i] = fmaf(k[i][c], k[i][c], n[8 + i]);
+      }
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) {
-      const bool up = lane & (2 * o);
+      for (int o = 8; o > 0; o >>= 1) {
+        const bool up = lane & (2 * o);
 #pragma unroll
-      for (int i = 0; i < o; ++i) {
-        const float keep = up ? n[i + o] : n[i], send = up ? n[i] : n[i + o];
-        n[i] = keep + __shfl_xor_sync(0xffffffffu, send, 2 * o);
+        for (int i = 0; i < o; ++i) {
+          const float keep = up ? n[i + o] : n[i], send = up ? n[i] : n[i + o];
+          n[i] = keep + __shfl_xor_sync(0xffffffffu, send, 2 * o);
+        }
+      }
+      sum = n[0] + __shfl_xor_sync(0xffffffffu, n[0], 1);
+      if (pass == kNormPasses || !__any_sync(0xffffffffu, sum == INFINITY)) break;
+      const float down = sum == INFINITY ? kNormDown : 1.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float dq = __shfl_sync(0xffffffffu, down, 2 * i), dk = __shfl_sync(0xffffffffu, down, 16 + 2 * i);
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) q[i][c] *= dq, k[i][c] *= dk;
       }
     }
-    const float r = 1.f / sqrtf(n[0] + __shfl_xor_sync(0xffffffffu, n[0], 1) + kNormEps);
+    const float r = 1.f / sqrtf(sum + kNormEps);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float rq = __shfl_sync(0xffffffffu, r, 2 * i), rk = __shfl_sync(0xffffffffu, r, 16 + 2 * i);
