@@ -532,9 +532,13 @@ int ling_moe_delta_test_set_wait(ling_moe_delta_t *h, int skip, uint64_t wait_li
  *   c_w + z_w[t] - log(sum_j exp(z_w[j])),
  * and for a finished beam the one candidate (eos, c_w).  The W best become the
  * group's beams, best first; ties go to the lower beam, then (inside a beam
- * the larger logit, then) the lower token.  Scores are formed in 64 bits and
- * rounded to fp32 once.  A logit of -inf or NaN is no candidate; a row whose
- * logits are all that, or hold +inf, has none.  Places that no candidate is
+ * the larger logit, then) the lower token.  The terms exp(z - max) are fp32 (2
+ * ulp, of differences rounded to fp32) and their sums fp32 with compensation and
+ * 64 bits, which leaves log sum exp off by some 2e-6 whatever the vocabulary;
+ * scores are formed from it in 64 bits and rounded to fp32 once.  So candidates
+ * of different beams whose scores lie closer than that may change places; those
+ * of one beam come in the order of their logits.  A logit of -inf or NaN is no
+ * candidate; a row whose logits are all that, or hold +inf, has none.  Places that no candidate is
  * left for get token -1, their own place as parent, score -inf, finished 1. */
 typedef struct ling_moe_beam ling_moe_beam_t; /* opaque handle: the selection's workspace */
 

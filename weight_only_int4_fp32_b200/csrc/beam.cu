@@ -3,10 +3,11 @@
 // Selection.  For group g, beam w with accumulated score c_w and logits z:
 //   candidate (w, t):  c_w + z_t - log sum_j exp(z_j)     (a live beam)
 //   candidate (w, eos): c_w                               (a finished beam)
-// and the W best candidates of the group in order.  Scores are formed in 64
-// bits (fp32 terms exp(z - max), summed in fp32 per thread over at most a few
-// hundred terms and in 64 bits above that), so that two beams' candidates
-// compare by more than the 2^-24 of an fp32 score; they are rounded to fp32
+// and the W best candidates of the group in order.  Terms exp(z - m) are fp32
+// (each off by (|z - m| + 4) 2^-23 of itself at most); a thread adds the 16 or 32
+// of a tile in fp32 and the tiles with compensation, threads and pieces join in 64
+// bits: log sum exp is off by 6e-7 and the terms' mean error, some 2e-6 in all,
+// however long the row.  Scores are formed from it in 64 bits and rounded to fp32
 // once, at the end.  Inside a row the order of the candidates is that of the
 // logits themselves, ties to the lower token, whatever the scores round to.
 //
@@ -234,8 +235,11 @@ __global__ void __launch_bounds__(kThreads, kBeamCtas) beam_select_kernel(const 
       sm.chosen = 0;
       sm.tau = kNoKey;
     }
-    // ---- one pass: the thread's largest logit and its sum of exp
-    float m = kLowest, s = 0.f, top = -INFINITY;
+    // ---- one pass: the thread's largest logit and its sum of exp(logit - m).  m follows the
+    // largest only when that is more than 1 above it, so that what a rescaling rounds has
+    // shrunk by e: however many there are, they add 2^-22 (1 + 1 / e + ...) at most.  s - low
+    // is the sum, each tile's added with compensation.
+    float m = kLowest, s = 0.f, low = 0.f, top = -INFINITY;
     {
       uint4 cur[NV], nxt[NV];
       load_tile<BF16>(cur, z, begin, end, tid, al);
@@ -243,9 +247,12 @@ __global__ void __launch_bounds__(kThreads, kBeamCtas) beam_select_kernel(const 
         if (base + kBeamTile < end) load_tile<BF16>(nxt, z, base + kBeamTile, end, tid, al);
         const float mx = Tile<BF16>::max(cur);
         top = fmaxf(top, mx);
-        const float mn = fmaxf(m, mx);
-        s *= exp_neg(m - mn);
-        m = mn;
+        if (mx > m + 1.f) {
+          const float f = exp_neg(m - mx);
+          s *= f;
+          low *= f;
+          m = mx;
+        }
         f2 t[2] = {0ull, 0ull};
         const f2 off = pack2(-m, -m), scale = pack2(kLog2e, kLog2e);
 #pragma unroll
@@ -264,7 +271,10 @@ __global__ void __launch_bounds__(kThreads, kBeamCtas) beam_select_kernel(const 
             for (int e = 0; e < VE; ++e) sum += exp_neg(fmaxf(Tile<BF16>::get(one, e), -INFINITY) - m);
           }
         }
-        s += sum;
+        sum -= low;
+        const float t2 = s + sum;
+        low = (t2 - s) - sum;
+        s = t2;
 #pragma unroll
         for (int v = 0; v < NV; ++v) cur[v] = nxt[v];
       }
@@ -388,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, kBeamCtas) beam_select_kernel(const 
     bm = sm.red_m[0];
 #pragma unroll
     for (int i = 1; i < kThreads / 32; ++i) bm = fmaxf(bm, sm.red_m[i]);
-    double ds = (double)s * (double)expf(m - bm);
+    double ds = ((double)s - (double)low) * (double)expf(m - bm);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ds += __shfl_xor_sync(0xffffffffu, ds, o);
     if (lane == 0) sm.red_s[warp] = ds;

@@ -15,8 +15,8 @@ constexpr int beam_tile(bool bf16) { return bf16 ? 8192 : 4096; }  // logits a C
 constexpr int kBeamCtas = 4;        // CTAs of the selection that an SM holds at once
 constexpr int kReorderTensors = 32; // tensors per reorder launch
 
-// One piece of a row: its largest logit, sum of exp(logit - max), and its best
-// keys in order (0: none).  Key: order key of the logit above ~token.
+// One piece of a row: max, at most 1 below its largest logit, the sum of
+// exp(logit - max), and its best keys in order (0: none).  Key: order key of the logit above ~token.
 struct BeamPart {
   double sum;
   float max;
