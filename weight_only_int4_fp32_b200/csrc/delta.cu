@@ -1118,7 +1118,10 @@ __global__ void __launch_bounds__(ScanCfg<DK>::kThreads, 1) delta_scan_kernel(co
   uint4* xu = reinterpret_cast<uint4*>(dsm + C::oU + mt * C::kXU);
   float* fs = reinterpret_cast<float*>(dsm + C::oFs) + mt * 32;
   float* fu = reinterpret_cast<float*>(dsm + C::oFu) + mt * 32;
-  auto pair_sync = [&] { asm volatile("bar.sync %0, 64;" :: "r"(mt + 1) : "memory"); };
+  auto pair_sync = [&] {
+    __syncwarp();
+    asm volatile("bar.sync %0, 64;" :: "r"(mt + 1) : "memory");
+  };
   bool dead = false;  // a wait ran out: no further waits, the results are void
   // U~ of this warp's tokens: 4 tiles of 8
   const unsigned char* ut = rec0 + C::kOps + (((size_t)(split * MT + mt) * 8 + 4 * hf) * 32 + lane) * 16;
@@ -1156,7 +1159,8 @@ __global__ void __launch_bounds__(ScanCfg<DK>::kThreads, 1) delta_scan_kernel(co
       }
     }
     pair_sync();
-    if (!dead) dead = !mbar_wait(full + b, (c >> 1) & 1, p.wait_ns, p.err);
+    // one answer for the warp: warp-wide instructions follow
+    if (!dead) dead = !mbar_wait_warp(full + b, (c >> 1) & 1, p.wait_ns, p.err);
     // ---- U^T and the state's part of O^T for this half of the tokens
     float U[4][4], O[4][4];
 #pragma unroll
@@ -1293,6 +1297,7 @@ __global__ void __launch_bounds__(ScanCfg<DK>::kThreads, 1) delta_scan_kernel(co
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(empty + b);  // the record is read
+    __syncwarp();
     // ---- out: 8 x 8 tiles turned, so that a lane has two columns of one token
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
