@@ -233,6 +233,7 @@ __global__ void __launch_bounds__(kGemvWarps * 32, 2) f8_gemv_kernel(const F8Par
       if (qi >= pairs) break;
       fetch();
     }
+    __syncwarp();  // the halves of a warp may leave after different rounds
     cluster_arrive();
     cluster_wait();
   } else {
