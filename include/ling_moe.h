@@ -439,9 +439,13 @@ int ling_moe_fp8_linear_test_set_wait(ling_moe_fp8_linear_t *h, int skip_cta, ui
  * g > 0 counts as 0; -inf forgets everything.  0 <= beta <= 2 (beyond that the
  * recurrence itself may grow without bound and a prefill's terms may overflow).
  * States are held and returned in fp32: the step computes in fp32, a prefill
- * takes two fp16 terms of each operand that feeds the state (about 22 bits);
- * operands that feed only the bf16 output take one.  Non-finite inputs spoil their own
- * sequence and head only. */
+ * takes two fp16 terms of each operand that feeds the state (about 22 bits, and
+ * 2^-35 of a token's largest at the least) after the decay that a token's channels
+ * share, its slowest one, has been taken out, which it carries in fp32: what strong
+ * decays leave of a state or of early writes keeps its precision, as long as the
+ * channels decay alike.  Operands that feed only the bf16 output take one term (2^-11,
+ * and a write reaches the outputs of its own 64 tokens to 2^-35 of itself at the least).
+ * Non-finite inputs spoil their own sequence and head only. */
 typedef struct {
   int k_heads, v_heads;  /* v_heads a multiple of k_heads */
   int head_k, head_v;    /* 64 or 128 each */
@@ -472,7 +476,7 @@ typedef struct {
 typedef struct ling_moe_delta ling_moe_delta_t; /* opaque handle: the prefill's workspace */
 
 /* Checks cfg and allocates the workspace on the current device: a record of up
- * to 123 KB per 64 tokens and head of a prefill, at most 16 per SM (292 MB with
+ * to 124 KB per 64 tokens and head of a prefill, at most 16 per SM (293 MB with
  * 128 x 128 states; one segment of chunks at least).  Synchronises the device.  As with every handle, one must
  * not be used by two streams (or two captured graphs that run at the same
  * time), and its calls belong to its device.

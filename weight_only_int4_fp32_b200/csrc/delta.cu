@@ -18,14 +18,23 @@
 // delta_prep_kernel forms, for every chunk and head at once, the operands
 // that do not depend on the state; delta_scan_kernel walks a sequence's
 // chunks with the state in registers.  Every decay is a product of factors
-// exp(g) <= 1 between two tokens, never a quotient, so that no decay, however
-// strong, overflows.
+// exp(g) <= 1 between two tokens, never a quotient below 2^-16, so that no decay,
+// however strong, overflows.
+//
+// A token's slowest decay, that of its largest log-decay over the channels, is
+// shared by all of them: the operands hold what the channels decay beyond it, and
+// the products of the slowest decays are fp32 factors of tokens, on the way into
+// and out of the tensor cores (W and q: from the chunk's start; U: to its end; B:
+// between its tokens; A, on U~'s side of the solution: through block borders).
+// So what a chunk leaves of early writes or of its first state, however little
+// that is where nothing is written after them, keeps its relative precision.
 //
 // Precision: products run on mma.sync with fp16 operands and fp32 sums.  What
 // feeds the state (fp32) is split into two fp16 terms (22 bits) after a power-
 // of-two scale taken from each row's largest value (fixed where the values are
-// bounded), three products per pair of split operands; what feeds only the bf16
-// output takes one fp16 term (half a step 2^-11, the output's own being 2^-8).
+// bounded: there the terms end at 2^-35), three products per pair of split operands; what
+// feeds only the bf16 output takes one fp16 term (half a step 2^-11, the output's own
+// being 2^-8; B's ends at 2^-35 too).
 #include "common.cuh"
 #include "delta.h"
 
@@ -33,7 +42,11 @@ namespace lingmoe {
 
 namespace {
 
-constexpr float kOpScale = 1024.f;  // k, q, T and B operands are stored times 2^10
+constexpr float kOpScale = 1024.f;  // operands that are 2 at most are stored times 2^10
+// A 16-row block's slowest decays in all, below which U~ is solved for without dividing by them:
+// of what is split after that division, the first rows keep 2^-38 / 2^-16 of the last ones.
+constexpr float kSteep = 0x1p-16f;
+constexpr float kTopScale = 8192.f;  // block_scale brings the largest value to 2^13 at least
 constexpr float kNormEps = 1e-6f;
 // A row whose sum of squares passes fp32 is taken times 2^-40, twice at most: 128 of the largest
 // bf16 numbers, 2^88 and then 2^48, and the sum stays above 2^48, beside which the 1e-6 is nothing.
@@ -481,9 +494,10 @@ __global__ void __launch_bounds__(256, 2) delta_step_kernel(const DeltaParams p)
 //
 // The record of a chunk and head: W^T hi, lo in the order of the B operands that
 // it becomes | q exp(G) [64][dk] | k exp(G_last - G) hi, lo [64][dk] | B [64][64] |
-// exp(G_last) fp32 [dk] | U~^T fp32 in the order of the accumulators that take it.
-// fp16 rows have their 16-byte
-// pieces exchanged, piece ^= row % 8, for conflict-free ldmatrix.
+// exp(G_last) fp32 [dk] | each token's slowest decays from the chunk's start [64] and
+// to its end, times k's power of two [64] | U~^T fp32 in the order of the accumulators that take
+// it.  W, q and k without the slowest decays.  fp16 rows have their 16-byte pieces
+// exchanged, piece ^= row % 8, for conflict-free ldmatrix.
 //
 // 56 us for 576 records of 128 x 128 heads (81 KB read, 123 KB written each): two
 // CTAs per SM (shared memory, 128 registers), whose own loads and dependent
@@ -503,7 +517,12 @@ struct PrepCfg {
   static constexpr int oT = oQ8 + kDeltaChunk / 2 * kHRow;                         // t [8][DK]
   static constexpr int oBefore = oT + 8 * DK * 4;                                  // [8][DK]
   static constexpr int oB = oBefore + 8 * DK * 4, oInfo = oB + 256;
-  static constexpr int kSmem = oInfo + 32;
+  // the slowest channel's decays: each token's, their products from the start of its 8-row block
+  // and behind it to the end, the blocks' whole; the same from the start of its 16-row
+  // block, beta over that, and the powers of two of k's blocks
+  static constexpr int oE = oInfo + 32, oEp = oE + 256, oEs = oEp + 256, oP = oEs + 256, oBp = oP + 256;
+  static constexpr int oEt = oBp + 256, oPk = oEt + 32;
+  static constexpr int kSmem = oPk + 32;
   // once the products are done: A and B in place of k s, v in place of q p, then
   // A's blocks below the diagonal and the inverses on it as fp16 in place of B
   static constexpr int oA = oKs, oBm = oKs + kMat, oV = oQ, oA16 = oBm;
@@ -531,6 +550,158 @@ __device__ __forceinline__ float quad_max(float m) {
   return fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
 }
 
+// 16 columns of W or U~ (`tile`): one warp, from a CTA's shared memory to its record.  U~'s
+// rows of a 16-row block are taken over the shared decay P from the block's start, and
+// multiplied by that in the end.  Where P gets steep (STEEP, U~ only), the inverses on
+// the diagonal, whose entries then fall with the decays as the rows of the result
+// do where nothing is written, are applied in fp32 instead.
+template <int DK, bool STEEP>
+__device__ __forceinline__ void solve_tile(unsigned char* dsm, unsigned char* rec, int tile) {
+  using C = PrepCfg<DK>;
+  const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
+  const float* skp = reinterpret_cast<const float*>(dsm + C::oKp);
+  const float* sbefore = reinterpret_cast<const float*>(dsm + C::oBefore);
+  const float* sbeta = reinterpret_cast<const float*>(dsm + C::oB);
+  const float* sEs = reinterpret_cast<const float*>(dsm + C::oEs);
+  const float* sEt = reinterpret_cast<const float*>(dsm + C::oEt);
+  const float* sP = reinterpret_cast<const float*>(dsm + C::oP);
+  const float* sBp = reinterpret_cast<const float*>(dsm + C::oBp);
+  const float* mA = reinterpret_cast<const float*>(dsm + C::oA);
+  const uint32_t a16 = smem_u32(dsm + C::oA16);
+  const int brow = (lane & 7) + ((lane >> 4) << 3), bpc = (lane >> 3) & 1;  // ldmatrix rows and pieces of a 16 x 16 block
+  const bool is_w = !STEEP && tile < DK / 16;
+  auto store_u = [&](int i, const float z[2][4]) {
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+      *reinterpret_cast<float4*>(rec + delta_ops_bytes(DK) + ((((tile - DK / 16) * 8 + 2 * i + nt) * 32 + lane) << 4)) =
+          make_float4(z[nt][0], z[nt][1], z[nt][2], z[nt][3]);
+  };
+  const int c = 16 * (is_w ? tile : tile - DK / 16) + gq;  // column of rows 0, 1 of the accumulators; + 8 of 2, 3
+  uint32_t fh[3][4], fl[3][4];
+  float f[3][2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float* scale = is_w || STEEP ? sbeta : sBp;
+    float y[2][4];
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int n = 16 * i + 8 * nt + 2 * tq + (e & 1), cc = c + (e >= 2 ? 8 : 0);
+        const float x = is_w ? skp[n * C::kFRow + cc] * sbefore[(2 * i + nt) * DK + cc]
+                             : __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(dsm + C::oV + n * C::kVRow + 2 * cc));
+        y[nt][e] = x * scale[n];
+      }
+    uint32_t bh[4], bl[4];
+#pragma unroll
+    for (int j = 0; j < i; ++j) {
+      const uint32_t at = a16 + (16 * i + brow) * 128 + (((2 * j + bpc) ^ (brow & 7)) << 4);
+      ldsm_a(at, bh);
+      ldsm_a(at + 8192, bl);
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+        mma(d, fh[j], bh[2 * nt], bh[2 * nt + 1]);
+        mma(d, fl[j], bh[2 * nt], bh[2 * nt + 1]);
+        mma(d, fh[j], bl[2 * nt], bl[2 * nt + 1]);
+        if constexpr (STEEP) {
+          const float2 r = *reinterpret_cast<const float2*>(sP + 16 * i + 8 * nt + 2 * tq);
+          d[0] *= r.x, d[1] *= r.y, d[2] *= r.x, d[3] *= r.y;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[nt][e] = fmaf(-f[j][e >> 1], d[e], y[nt][e]);
+      }
+    }
+    // the block's inverse times y, and the block as the next ones' operand
+    float s0, s1, i0, i1, w[2][4];
+    uint32_t oh[4], ol[4];
+    if constexpr (STEEP) {
+      float z[2][4];
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[nt][e] = 0.f;
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int o = 0; o < 4; ++o) {  // tokens 8 half + 2 o, + 1, which lane o of the quad holds
+          float x[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = __shfl_sync(0xffffffffu, y[half][e], (lane & 28) | o);
+#pragma unroll
+          for (int nt = half; nt < 2; ++nt)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const float2 t = *reinterpret_cast<const float2*>(mA + (16 * i + 8 * nt + 2 * tq + b) * C::kMRow + 16 * i +
+                                                                8 * half + 2 * o);
+              w[nt][b] = fmaf(t.x, x[0], fmaf(t.y, x[1], w[nt][b]));
+              w[nt][2 + b] = fmaf(t.x, x[2], fmaf(t.y, x[3], w[nt][2 + b]));
+            }
+        }
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {  // decayed to the block's end
+          const int n = 16 * i + 8 * nt + 2 * tq + (e & 1);
+          z[nt][e] = w[nt][e];
+          w[nt][e] *= sEs[n] * (nt ? 1.f : sEt[2 * i + 1]);
+        }
+      store_u(i, z);
+    } else {
+      uint32_t yh[4], yl[4];
+      block_scale(quad_max(fmaxf(fmaxf(fabsf(y[0][0]), fabsf(y[0][1])), fmaxf(fabsf(y[1][0]), fabsf(y[1][1])))), s0, i0);
+      block_scale(quad_max(fmaxf(fmaxf(fabsf(y[0][2]), fabsf(y[0][3])), fmaxf(fabsf(y[1][2]), fabsf(y[1][3])))), s1, i1);
+      split_frag(y[0], y[1], s0, s1, yh, yl);
+      const uint32_t at = a16 + (16 * i + brow) * 128 + (((2 * i + bpc) ^ (brow & 7)) << 4);
+      ldsm_a(at, bh);
+      ldsm_a(at + 8192, bl);
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+        mma(d, yh, bh[2 * nt], bh[2 * nt + 1]);
+        mma(d, yl, bh[2 * nt], bh[2 * nt + 1]);
+        mma(d, yh, bl[2 * nt], bl[2 * nt + 1]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[nt][e] = d[e] * ((e >= 2 ? i1 : i0) * (1.f / kOpScale));
+      }
+      if (!is_w) {
+        float z[2][4];
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          const float2 r = *reinterpret_cast<const float2*>(sP + 16 * i + 8 * nt + 2 * tq);
+          z[nt][0] = w[nt][0] * r.x, z[nt][1] = w[nt][1] * r.y, z[nt][2] = w[nt][2] * r.x, z[nt][3] = w[nt][3] * r.y;
+        }
+        store_u(i, z);
+      }
+    }
+    if (is_w) {  // W's terms are the record's
+      s0 = s1 = kOpScale;
+      i0 = i1 = 1.f / kOpScale;
+    } else {
+      block_scale(quad_max(fmaxf(fmaxf(fabsf(w[0][0]), fabsf(w[0][1])), fmaxf(fabsf(w[1][0]), fabsf(w[1][1])))), s0, i0);
+      block_scale(quad_max(fmaxf(fmaxf(fabsf(w[0][2]), fabsf(w[0][3])), fmaxf(fabsf(w[1][2]), fabsf(w[1][3])))), s1, i1);
+    }
+    split_frag(w[0], w[1], s0, s1, oh, ol);
+    if (is_w) {  // 8 x 8 tiles turned: the B operand of 16 channels and tokens 16 i ..
+      uint4* dst = reinterpret_cast<uint4*>(rec) + (tile * 4 + i) * 32 + lane;
+      *dst = make_uint4(turn8(oh[0]), turn8(oh[1]), turn8(oh[2]), turn8(oh[3]));
+      dst[delta_tile_bytes(DK) / 16] = make_uint4(turn8(ol[0]), turn8(ol[1]), turn8(ol[2]), turn8(ol[3]));
+    }
+    if (i < 3) {
+#pragma unroll
+      for (int m = 0; m < 4; ++m) fh[i][m] = oh[m], fl[i][m] = ol[m];
+      // decayed to where the next block starts: this block's whole, unless that is in w
+      const float t = is_w || STEEP ? 1.f : sP[16 * i + 15];
+      f[i][0] = i0 * (1.f / kOpScale) * t;
+      f[i][1] = i1 * (1.f / kOpScale) * t;
+      if (!is_w) {
+#pragma unroll
+        for (int j = 0; j < i; ++j) f[j][0] *= sP[16 * i + 15], f[j][1] *= sP[16 * i + 15];
+      }
+    }
+  }
+}
+
 template <int DK>
 __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p) {
   using C = PrepCfg<DK>;
@@ -542,6 +713,13 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
   float* sbefore = reinterpret_cast<float*>(dsm + C::oBefore);
   float* sbeta = reinterpret_cast<float*>(dsm + C::oB);
   int* info = reinterpret_cast<int*>(dsm + C::oInfo);
+  float* sE = reinterpret_cast<float*>(dsm + C::oE);
+  float* sEp = reinterpret_cast<float*>(dsm + C::oEp);
+  float* sEs = reinterpret_cast<float*>(dsm + C::oEs);
+  float* sEt = reinterpret_cast<float*>(dsm + C::oEt);
+  float* sP = reinterpret_cast<float*>(dsm + C::oP);
+  float* sBp = reinterpret_cast<float*>(dsm + C::oBp);
+  float* spk = reinterpret_cast<float*>(dsm + C::oPk);
   float* mA = reinterpret_cast<float*>(dsm + C::oA);
   float* mB = reinterpret_cast<float*>(dsm + C::oBm);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -638,8 +816,38 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
       for (int c = 0; c < CPL; ++c) {
         q[i][c] *= rq;
         k[i][c] *= rk;
-        a[i][c] = decay_of(a[i][c]);
       }
+    }
+    // each token's slowest decay (e^-200 is 0), and the channels' beyond it
+    float mine = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float m = INFINITY;
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) {
+        a[i][c] = a[i][c] > 0.f ? 0.f : a[i][c];
+        m = fminf(m, fabsf(a[i][c]));
+      }
+      const float slow = fminf(__uint_as_float(__reduce_min_sync(0xffffffffu, __float_as_uint(m))), 200.f);
+      if (lane == i) mine = slow;
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) a[i][c] = expf(a[i][c] + slow);
+    }
+    // lane i < 8: products of the slowest decays up to token i, and behind it
+    const float e = expf(-mine);
+    float ep = e, es = e;
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+      const float x = __shfl_up_sync(0xffffffffu, ep, o, 8), y = __shfl_down_sync(0xffffffffu, es, o, 8);
+      if ((lane & 7) >= o) ep *= x;
+      if ((lane & 7) + o < 8) es *= y;
+    }
+    es = __shfl_down_sync(0xffffffffu, es, 1, 8);
+    if (lane < 8) {
+      sE[row0 + lane] = e;
+      sEp[row0 + lane] = ep;
+      sEs[row0 + lane] = lane < 7 ? es : 1.f;
+      if (lane == 7) sEt[warp] = ep;
     }
   }
   auto store_row = [&](float* dst, const float* x) {
@@ -648,12 +856,11 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
     else
       *reinterpret_cast<float2*>(dst) = make_float2(x[0], x[1]);
   };
-  auto store_half = [&](unsigned char* dst, const float* x) {  // times the operands' scale
+  auto store_half = [&](unsigned char* dst, const float* x, float s) {
     if constexpr (CPL == 4)
-      *reinterpret_cast<uint2*>(dst) =
-          make_uint2(pack_half2(x[0] * kOpScale, x[1] * kOpScale), pack_half2(x[2] * kOpScale, x[3] * kOpScale));
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_half2(x[0] * s, x[1] * s), pack_half2(x[2] * s, x[3] * s));
     else
-      *reinterpret_cast<uint32_t*>(dst) = pack_half2(x[0] * kOpScale, x[1] * kOpScale);
+      *reinterpret_cast<uint32_t*>(dst) = pack_half2(x[0] * s, x[1] * s);
   };
   // k p and k s; the block's whole product; q p of a tile's second half (for its border)
   {
@@ -668,7 +875,7 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
       if (warp & 1) {
 #pragma unroll
         for (int c = 0; c < CPL; ++c) y[c] = q[i][c] * x[c];
-        store_half(dsm + C::oQ8 + (8 * (warp >> 1) + i) * C::kHRow + 2 * c0, y);
+        store_half(dsm + C::oQ8 + (8 * (warp >> 1) + i) * C::kHRow + 2 * c0, y, kOpScale);
       }
     }
     store_row(st + warp * DK + c0, x);
@@ -731,6 +938,14 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
         if (w > warp) after[c] *= t;
       }
     store_row(sbefore + warp * DK + c0, before);
+    // k's operand is scaled by what its block decays to the end at least
+    float sk, ik, mk = 0.f;
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) mk = fmaxf(mk, after[c]);
+    block_scale(warp_max_abs(mk), sk, ik);
+    if (lane == 0) spk[warp] = ik * kTopScale;
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) after[c] *= sk;
     float x[CPL], first[CPL];
 #pragma unroll
     for (int c = 0; c < CPL; ++c) {
@@ -749,10 +964,10 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
         const float y = q[i][c] * x[c];
         qt[c] = y * before[c];
         qp[c] = y * first[c];
-        kh[c] = after[c] * kOpScale * sks[r * C::kFRow + c0 + c];
+        kh[c] = after[c] * sks[r * C::kFRow + c0 + c];
       }
-      store_half(dsm + C::oQ + r * C::kHRow + 2 * c0, qp);
-      store_half(rec + 2 * KT + at, qt);
+      store_half(dsm + C::oQ + r * C::kHRow + 2 * c0, qp, kOpScale);
+      store_half(rec + 2 * KT + at, qt, kOpScale);
       uint32_t hi[CPL / 2], lo[CPL / 2];
 #pragma unroll
       for (int c = 0; c < CPL / 2; ++c) split2(kh[2 * c], kh[2 * c + 1], hi[c], lo[c]);
@@ -764,14 +979,33 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
         *reinterpret_cast<uint32_t*>(rec + 4 * KT + at) = lo[0];
       }
     }
-    if (warp == 7) {  // nothing after the last block: exp(G_last) = before x its own product
-      float y[CPL];
-#pragma unroll
-      for (int c = 0; c < CPL; ++c) y[c] = before[c] * st[7 * DK + c0 + c];
-      store_row(reinterpret_cast<float*>(rec + 5 * KT + kDeltaChunk * kDeltaChunk * 2) + c0, y);
-    }
   }
   __syncthreads();
+  // the record's factors, those of the solution
+  if (tid < DK) {
+    float* f = reinterpret_cast<float*>(rec + 5 * delta_tile_bytes(DK) + kDeltaChunk * kDeltaChunk * 2);
+    float all = 1.f;
+    if (tid < kDeltaChunk) {
+      const int w = tid >> 3;
+      float up = 1.f, down = 1.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float t = sEt[i];
+        all *= t;
+        if (i < w - (w & 1)) up *= t;
+        if (i > w) down *= t;
+      }
+      const float x = sEp[tid] * (w & 1 ? sEt[w - 1] : 1.f);
+      sP[tid] = x;
+      sBp[tid] = sbeta[tid] / x;
+      f[DK + tid] = x * up;
+      f[DK + 64 + tid] = sEs[tid] * down * spk[w];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) all *= sEt[i];
+    }
+    f[tid] = sbefore[7 * DK + tid] * st[7 * DK + tid] * all;
+  }
 
   // ---- tile row a of A and B, half the channels per warp
   const int ta = warp & 3, hh = warp >> 2, gq = lane >> 2, tq = lane & 3;
@@ -855,6 +1089,18 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
   }
   __syncthreads();
   constexpr float kUn = 1.f / (kOpScale * kOpScale);
+  {  // B's slowest decays: from the column to its block's end, from there to the row
+    float d0 = sP[16 * ta + gq] * kUn, d1 = sP[16 * ta + gq + 8] * kUn;
+#pragma unroll
+    for (int u = 0; u < 7; ++u) {
+      const int s = u == 6 ? 2 * ta : 2 * ta - 1 - u;
+      if (s < 0) continue;
+      const float2 x = *reinterpret_cast<const float2*>(sEs + 8 * s + 2 * tq);
+      if (u == 6) d1 = sEp[16 * ta + gq + 8] * kUn;
+      accB[u][0] *= d0 * x.x, accB[u][1] *= d0 * x.y, accB[u][2] *= d1 * x.x, accB[u][3] *= d1 * x.y;
+      d0 *= sEt[s], d1 *= sEt[s];
+    }
+  }
 #pragma unroll 1
   for (int turn = 0; turn < 2; ++turn) {
     if (hh == turn) {
@@ -867,7 +1113,7 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
           const int r = 16 * ta + gq + (e >= 2 ? 8 : 0), c = 8 * s + 2 * tq + (e & 1);
           if (u == 6 && e < 2) continue;
           mA[r * C::kMRow + c] += accA[u][e] * (kUn * sbeta[r]);
-          mB[r * C::kMRow + c] += accB[u][e] * kUn;
+          mB[r * C::kMRow + c] += accB[u][e];
         }
       }
     }
@@ -877,7 +1123,10 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
         while (i * (i + 1) / 2 <= lane) ++i;
         j = lane - i * (i - 1) / 2;
         mA[(row0 + i) * C::kMRow + row0 + j] = dkk * sbeta[row0 + i];
-        mB[(row0 + i) * C::kMRow + row0 + j] = dqk;
+        float d = dqk;
+#pragma unroll
+        for (int m = 1; m < 8; ++m) d *= j + m <= i ? sE[row0 + j + m] : 1.f;
+        mB[(row0 + i) * C::kMRow + row0 + j] = d;
       } else {
         i = row0 + lane - 28;
         mB[i * C::kMRow + i] = dkk;
@@ -934,87 +1183,25 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
   }
   __syncthreads();
 
-  // ---- the solution, 16 columns of W or U~ at a time
-  const uint32_t a16 = smem_u32(dsm + C::oA16);
-  const int brow = (lane & 7) + ((lane >> 4) << 3), bpc = (lane >> 3) & 1;  // ldmatrix rows and pieces of a 16 x 16 block
+  // ---- where a block's decay is steep: the inverses times the decays between their tokens,
+  // a row of a block and four of its columns per thread
+  const bool steep = fminf(fminf(sP[15], sP[31]), fminf(sP[47], sP[63])) < kSteep;
+  if (steep) {
+    const int r = tid >> 2, c0 = (r & 48) + 4 * (tid & 3);
+    float d = 0.f;
+    for (int c = r; c >= c0; --c) {
+      d = c == r ? 1.f : d * sE[c + 1];
+      if (c < c0 + 4) mA[r * C::kMRow + c] *= d;
+    }
+    __syncthreads();
+  }
+  // ---- the solution, 16 columns at a time
 #pragma unroll 1
   for (int tile = warp; tile < (DK + p.dv) / 16; tile += 8) {
-    const bool is_w = tile < DK / 16;
-    const int c = 16 * (is_w ? tile : tile - DK / 16) + gq;  // column of rows 0, 1 of the accumulators; + 8 of 2, 3
-    uint32_t fh[3][4], fl[3][4];
-    float f[3][2];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float y[2][4];
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int n = 16 * i + 8 * nt + 2 * tq + (e & 1), cc = c + (e >= 2 ? 8 : 0);
-          const float x = is_w ? skp[n * C::kFRow + cc] * sbefore[(2 * i + nt) * DK + cc]
-                               : __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(dsm + C::oV + n * C::kVRow + 2 * cc));
-          y[nt][e] = x * sbeta[n];
-        }
-      uint32_t bh[4], bl[4];
-#pragma unroll
-      for (int j = 0; j < i; ++j) {
-        const uint32_t at = a16 + (16 * i + brow) * 128 + (((2 * j + bpc) ^ (brow & 7)) << 4);
-        ldsm_a(at, bh);
-        ldsm_a(at + 8192, bl);
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          float d[4] = {0.f, 0.f, 0.f, 0.f};
-          mma(d, fh[j], bh[2 * nt], bh[2 * nt + 1]);
-          mma(d, fl[j], bh[2 * nt], bh[2 * nt + 1]);
-          mma(d, fh[j], bl[2 * nt], bl[2 * nt + 1]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) y[nt][e] = fmaf(-f[j][e >> 1], d[e], y[nt][e]);
-        }
-      }
-      float s0, s1, i0, i1;
-      uint32_t yh[4], yl[4];
-      block_scale(quad_max(fmaxf(fmaxf(fabsf(y[0][0]), fabsf(y[0][1])), fmaxf(fabsf(y[1][0]), fabsf(y[1][1])))), s0, i0);
-      block_scale(quad_max(fmaxf(fmaxf(fabsf(y[0][2]), fabsf(y[0][3])), fmaxf(fabsf(y[1][2]), fabsf(y[1][3])))), s1, i1);
-      split_frag(y[0], y[1], s0, s1, yh, yl);
-      const uint32_t at = a16 + (16 * i + brow) * 128 + (((2 * i + bpc) ^ (brow & 7)) << 4);
-      ldsm_a(at, bh);
-      ldsm_a(at + 8192, bl);
-      float w[2][4];
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
-        mma(d, yh, bh[2 * nt], bh[2 * nt + 1]);
-        mma(d, yl, bh[2 * nt], bh[2 * nt + 1]);
-        mma(d, yh, bl[2 * nt], bl[2 * nt + 1]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[nt][e] = d[e] * ((e >= 2 ? i1 : i0) * (1.f / kOpScale));
-      }
-      // the block as the next ones' operand; W's terms are the record's
-      uint32_t oh[4], ol[4];
-      if (is_w) {
-        s0 = s1 = kOpScale;
-        i0 = i1 = 1.f / kOpScale;
-      } else {
-        block_scale(quad_max(fmaxf(fmaxf(fabsf(w[0][0]), fabsf(w[0][1])), fmaxf(fabsf(w[1][0]), fabsf(w[1][1])))), s0, i0);
-        block_scale(quad_max(fmaxf(fmaxf(fabsf(w[0][2]), fabsf(w[0][3])), fmaxf(fabsf(w[1][2]), fabsf(w[1][3])))), s1, i1);
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-          *reinterpret_cast<float4*>(rec + delta_ops_bytes(DK) + ((((tile - DK / 16) * 8 + 2 * i + nt) * 32 + lane) << 4)) =
-              make_float4(w[nt][0], w[nt][1], w[nt][2], w[nt][3]);
-      }
-      split_frag(w[0], w[1], s0, s1, oh, ol);
-      if (is_w) {  // 8 x 8 tiles turned: the B operand of 16 channels and tokens 16 i ..
-        uint4* dst = reinterpret_cast<uint4*>(rec) + (tile * 4 + i) * 32 + lane;
-        *dst = make_uint4(turn8(oh[0]), turn8(oh[1]), turn8(oh[2]), turn8(oh[3]));
-        dst[delta_tile_bytes(DK) / 16] = make_uint4(turn8(ol[0]), turn8(ol[1]), turn8(ol[2]), turn8(ol[3]));
-      }
-      if (i < 3) {
-#pragma unroll
-        for (int m = 0; m < 4; ++m) fh[i][m] = oh[m], fl[i][m] = ol[m];
-        f[i][0] = i0 * (1.f / kOpScale);
-        f[i][1] = i1 * (1.f / kOpScale);
-      }
-    }
+    if (steep && tile >= DK / 16)
+      solve_tile<DK, true>(dsm, rec, tile);
+    else
+      solve_tile<DK, false>(dsm, rec, tile);
   }
   if (last) pdl_wait();
 }
@@ -1046,11 +1233,13 @@ struct ScanCfg {
   static constexpr int kOps = delta_ops_bytes(DK);
   static constexpr int kKs = DK / 32;                      // 16-channel steps of a half
   static constexpr int kXS = 2 * kKs * 2 * 512;            // a column tile's S^T operand: halves, steps, terms
-  static constexpr int kXU = 2 * 2 * 2 * 512;              // its U^T operand
+  static constexpr int kXU = 2 * 2 * 3 * 512;              // its U^T operands: decayed to the chunk's end, two terms; as it is, one
   static constexpr int oX = 2 * kOps, oU = oX + MT * kXS;
   static constexpr int oFs = oU + MT * kXU, oFu = oFs + MT * 2 * 16 * 4;  // inverse scales [MT][half][16]
-  static constexpr int oBar = oFu + MT * 2 * 16 * 4, oInfo = oBar + 4 * 8;
+  static constexpr int oFb = oFu + MT * 2 * 16 * 4;
+  static constexpr int oBar = oFb + MT * 2 * 16 * 4, oInfo = oBar + 4 * 8;
   static constexpr int kSmem = oInfo + 32;
+  static_assert(kSmem <= 232448, "two records and the operands exceed 227 KB of shared memory");
 };
 
 template <int DK>
@@ -1118,6 +1307,7 @@ __global__ void __launch_bounds__(ScanCfg<DK>::kThreads, 1) delta_scan_kernel(co
   uint4* xu = reinterpret_cast<uint4*>(dsm + C::oU + mt * C::kXU);
   float* fs = reinterpret_cast<float*>(dsm + C::oFs) + mt * 32;
   float* fu = reinterpret_cast<float*>(dsm + C::oFu) + mt * 32;
+  float* fb = reinterpret_cast<float*>(dsm + C::oFb) + mt * 32;
   auto pair_sync = [&] {
     __syncwarp();
     asm volatile("bar.sync %0, 64;" :: "r"(mt + 1) : "memory");
@@ -1136,6 +1326,9 @@ __global__ void __launch_bounds__(ScanCfg<DK>::kThreads, 1) delta_scan_kernel(co
   for (int c = 0; c < n; ++c) {
     const int b = c & 1;
     const uint32_t ops = base + b * C::kOps;
+    // exp(G_last) of the channels; of this half's tokens the factors of W and q, and of U
+    const float* dec = reinterpret_cast<const float*>(dsm + b * C::kOps + 5 * KT + kDeltaChunk * kDeltaChunk * 2);
+    const float* tokf = dec + DK + 32 * hf + 2 * tq;
     // ---- this half of S^T as operand
     {
       float m0 = 0.f, m1 = 0.f, s0, s1, i0, i1;
@@ -1161,17 +1354,12 @@ __global__ void __launch_bounds__(ScanCfg<DK>::kThreads, 1) delta_scan_kernel(co
     pair_sync();
     // one answer for the warp: warp-wide instructions follow
     if (!dead) dead = !mbar_wait_warp(full + b, (c >> 1) & 1, p.wait_ns, p.err);
-    // ---- U^T and the state's part of O^T for this half of the tokens
+    // ---- U^T and the state's part of O^T for this half of the tokens: W S0 and q S0 first
     float U[4][4], O[4][4];
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
-      U[nt][0] = un[nt].x, U[nt][1] = un[nt].y, U[nt][2] = un[nt].z, U[nt][3] = un[nt].w;
+      U[nt][0] = U[nt][1] = U[nt][2] = U[nt][3] = 0.f;
       O[nt][0] = O[nt][1] = O[nt][2] = O[nt][3] = 0.f;
-    }
-    if (c + 1 < n) {
-      ut += rec_step;
-#pragma unroll
-      for (int nt = 0; nt < 4; ++nt) un[nt] = __ldcg(reinterpret_cast<const float4*>(ut + nt * 512));
     }
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
@@ -1209,39 +1397,61 @@ __global__ void __launch_bounds__(ScanCfg<DK>::kThreads, 1) delta_scan_kernel(co
       for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          U[nt][e] = fmaf(-(e >= 2 ? f1 : f0), d[nt][e], U[nt][e]);
+          U[nt][e] = fmaf(e >= 2 ? f1 : f0, d[nt][e], U[nt][e]);
           O[nt][e] = fmaf(e >= 2 ? f1 : f0, o[nt][e], O[nt][e]);
         }
     }
-    // ---- this half of U^T as operand
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt) {
+      const float2 x = *reinterpret_cast<const float2*>(tokf + 8 * nt);
+      U[nt][0] = fmaf(-x.x, U[nt][0], un[nt].x), U[nt][1] = fmaf(-x.y, U[nt][1], un[nt].y);
+      U[nt][2] = fmaf(-x.x, U[nt][2], un[nt].z), U[nt][3] = fmaf(-x.y, U[nt][3], un[nt].w);
+      O[nt][0] *= x.x, O[nt][1] *= x.y, O[nt][2] *= x.x, O[nt][3] *= x.y;
+    }
+    if (c + 1 < n) {
+      ut += rec_step;
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt) un[nt] = __ldcg(reinterpret_cast<const float4*>(ut + nt * 512));
+    }
+    // ---- this half of U^T as operands: of the output as it is, of the state decayed to the end
     {
-      float m0 = 0.f, m1 = 0.f, s0, s1, i0, i1;
+      float V[4][4], m[4] = {0.f, 0.f, 0.f, 0.f}, sc[4], inv[4];
 #pragma unroll
       for (int nt = 0; nt < 4; ++nt) {
-        m0 = fmaxf(m0, fmaxf(fabsf(U[nt][0]), fabsf(U[nt][1])));
-        m1 = fmaxf(m1, fmaxf(fabsf(U[nt][2]), fabsf(U[nt][3])));
+        const float2 x = *reinterpret_cast<const float2*>(tokf + 64 + 8 * nt);
+        V[nt][0] = U[nt][0] * x.x, V[nt][1] = U[nt][1] * x.y, V[nt][2] = U[nt][2] * x.x, V[nt][3] = U[nt][3] * x.y;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          m[e] = fmaxf(m[e], fmaxf(fabsf(V[nt][2 * e]), fabsf(V[nt][2 * e + 1])));
+          m[2 + e] = fmaxf(m[2 + e], fmaxf(fabsf(U[nt][2 * e]), fabsf(U[nt][2 * e + 1])));
+        }
       }
-      block_scale(quad_max(m0), s0, i0);
-      block_scale(quad_max(m1), s1, i1);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) block_scale(quad_max(m[e]), sc[e], inv[e]);
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         uint32_t hi[4], lo[4];
-        split_frag(U[2 * ks], U[2 * ks + 1], s0, s1, hi, lo);
-        xu[((hf * 2 + ks) * 2 + 0) * 32 + lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        xu[((hf * 2 + ks) * 2 + 1) * 32 + lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        split_frag(V[2 * ks], V[2 * ks + 1], sc[0], sc[1], hi, lo);
+        xu[((hf * 2 + ks) * 3 + 0) * 32 + lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        xu[((hf * 2 + ks) * 3 + 1) * 32 + lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        const float* x = U[2 * ks];
+        const float* y = U[2 * ks + 1];
+        xu[((hf * 2 + ks) * 3 + 2) * 32 + lane] =
+            make_uint4(pack_half2(x[0] * sc[2], x[1] * sc[2]), pack_half2(x[2] * sc[3], x[3] * sc[3]),
+                       pack_half2(y[0] * sc[2], y[1] * sc[2]), pack_half2(y[2] * sc[3], y[3] * sc[3]));
       }
       if (tq == 0) {
-        fu[hf * 16 + gq] = i0 * (1.f / kOpScale);
-        fu[hf * 16 + gq + 8] = i1 * (1.f / kOpScale);
+        fu[hf * 16 + gq] = inv[0] * (1.f / kTopScale);
+        fu[hf * 16 + gq + 8] = inv[1] * (1.f / kTopScale);
+        fb[hf * 16 + gq] = inv[2] * (1.f / kOpScale);
+        fb[hf * 16 + gq + 8] = inv[3] * (1.f / kOpScale);
       }
     }
     pair_sync();
     // ---- S^T of this half of the channels, O^T of this half of the tokens
-    const float* dec = reinterpret_cast<const float*>(dsm + b * C::kOps + 5 * KT + kDeltaChunk * kDeltaChunk * 2) +
-                       hf * (DK / 2) + 2 * tq;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const float2 x = *reinterpret_cast<const float2*>(dec + 8 * nt);
+      const float2 x = *reinterpret_cast<const float2*>(dec + hf * (DK / 2) + 2 * tq + 8 * nt);
       S[nt][0] *= x.x, S[nt][1] *= x.y, S[nt][2] *= x.x, S[nt][3] *= x.y;
     }
 #pragma unroll
@@ -1257,7 +1467,7 @@ __global__ void __launch_bounds__(ScanCfg<DK>::kThreads, 1) delta_scan_kernel(co
         for (int e = 0; e < 4; ++e) o[nt][e] = 0.f;
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
-        const uint4 h4 = xu[((half * 2 + ks) * 2 + 0) * 32 + lane], l4 = xu[((half * 2 + ks) * 2 + 1) * 32 + lane];
+        const uint4 h4 = xu[((half * 2 + ks) * 3 + 0) * 32 + lane], l4 = xu[((half * 2 + ks) * 3 + 1) * 32 + lane];
         const uint32_t ah[4] = {h4.x, h4.y, h4.z, h4.w}, al[4] = {l4.x, l4.y, l4.z, l4.w};
         const int kr = 16 * (2 * half + ks);
         uint32_t kh[KS][4];
@@ -1270,6 +1480,8 @@ __global__ void __launch_bounds__(ScanCfg<DK>::kThreads, 1) delta_scan_kernel(co
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) mma(d[nt], ah, kh[nt >> 1][2 * (nt & 1)], kh[nt >> 1][2 * (nt & 1) + 1]);
         if (half <= hf) {  // B is lower triangular
+          const uint4 o4 = xu[((half * 2 + ks) * 3 + 2) * 32 + lane];
+          const uint32_t ao[4] = {o4.x, o4.y, o4.z, o4.w};
           uint32_t bh[2][4];
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
@@ -1277,7 +1489,7 @@ __global__ void __launch_bounds__(ScanCfg<DK>::kThreads, 1) delta_scan_kernel(co
             ldsm_a(ops + 5 * KT + r * 128 + (((kr / 8 + bpc) ^ (r & 7)) << 4), bh[g]);
           }
 #pragma unroll
-          for (int nt = 0; nt < 4; ++nt) mma(o[nt], ah, bh[nt >> 1][2 * (nt & 1)], bh[nt >> 1][2 * (nt & 1) + 1]);
+          for (int nt = 0; nt < 4; ++nt) mma(o[nt], ao, bh[nt >> 1][2 * (nt & 1)], bh[nt >> 1][2 * (nt & 1) + 1]);
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) mma(d[nt], al, kh[nt >> 1][2 * (nt & 1)], kh[nt >> 1][2 * (nt & 1) + 1]);
@@ -1286,6 +1498,7 @@ __global__ void __launch_bounds__(ScanCfg<DK>::kThreads, 1) delta_scan_kernel(co
         for (int nt = 0; nt < NT; ++nt) mma(d[nt], ah, kh[nt >> 1][2 * (nt & 1)], kh[nt >> 1][2 * (nt & 1) + 1]);
       }
       const float f0 = fu[half * 16 + gq], f1 = fu[half * 16 + gq + 8];
+      const float b0 = fb[half * 16 + gq], b1 = fb[half * 16 + gq + 8];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -1293,7 +1506,7 @@ __global__ void __launch_bounds__(ScanCfg<DK>::kThreads, 1) delta_scan_kernel(co
 #pragma unroll
       for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) O[nt][e] = fmaf(e >= 2 ? f1 : f0, o[nt][e], O[nt][e]);
+        for (int e = 0; e < 4; ++e) O[nt][e] = fmaf(e >= 2 ? b1 : b0, o[nt][e], O[nt][e]);
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(empty + b);  // the record is read

@@ -14,7 +14,9 @@ constexpr int kDeltaMaxStep = 8;   // tokens per sequence of a step
 
 // one chunk of one head: what the scan needs of q, k, v, g and beta (delta.cu)
 __host__ __device__ constexpr int delta_tile_bytes(int dk) { return kDeltaChunk * dk * 2; }
-__host__ __device__ constexpr int delta_ops_bytes(int dk) { return 5 * delta_tile_bytes(dk) + kDeltaChunk * kDeltaChunk * 2 + dk * 4; }
+__host__ __device__ constexpr int delta_ops_bytes(int dk) {
+  return 5 * delta_tile_bytes(dk) + kDeltaChunk * kDeltaChunk * 2 + (dk + 2 * kDeltaChunk) * 4;
+}
 __host__ __device__ constexpr int delta_rec_bytes(int dk, int dv) { return delta_ops_bytes(dk) + kDeltaChunk * dv * 4; }
 
 struct DeltaParams {
