@@ -441,9 +441,10 @@ int ling_moe_fp8_linear_test_set_wait(ling_moe_fp8_linear_t *h, int skip_cta, ui
  * States are held and returned in fp32: the step computes in fp32, a prefill
  * takes two fp16 terms of each operand that feeds the state (about 22 bits, and
  * 2^-35 of a token's largest at the least) after the decay that a token's channels
- * share, its slowest one, has been taken out, which it carries in fp32: what strong
- * decays leave of a state or of early writes keeps its precision, as long as the
- * channels decay alike.  Operands that feed only the bf16 output take one term (2^-11,
+ * share, its slowest one, has been taken out, which it carries in fp32, and with a
+ * scale of its own for each token's key: what strong decays leave of a state and of
+ * early writes keeps its precision where nothing corrects it (beta 0), and as long
+ * as the channels decay alike everywhere.  Operands that feed only the bf16 output take one term (2^-11,
  * and a write reaches the outputs of its own 64 tokens to 2^-35 of itself at the least).
  * Non-finite inputs spoil their own sequence and head only. */
 typedef struct {

@@ -82,3 +82,39 @@ def test_decays_from_none_to_all():
     base.close_out(base.np64(out), want, eo)
     base.close_state(base.np64(st[0]), states[-1], es)
     f.close()
+
+
+@pytest.mark.parametrize("dk", [64, 128])
+@pytest.mark.parametrize("T,rate,w", [(15, 6.0, 5), (30, 2.0, 5), (40, 1.5, 5), (64, 0.8, 5), (100, 0.5, 5), (8, 12.0, 5),
+                                      (8, 12.0, 1), (16, 5.0, 1), (60, 1.0, 1)])
+def test_first_writes_survive_whatever_the_channels_decay(T, rate, w, dk):
+    """w tokens write under mild decays; then every channel of every token decays at random and nothing is written,
+    so that all channels fall far below the slowest decays' product.  Those tokens' state has the error e of
+    oracle/delta_ref.py, of which each channel keeps its decays' part; a row of k exp(..) is off by
+    2^-22 and 360 u of itself and 2^-38 of its largest, its channels' decays once more by 360 u."""
+    H, dv = 2, 64
+    f = lm.GatedDeltaRule(H, H, dk, dv, T, 1)
+    cu = torch.tensor([0, T], dtype=torch.int32, device=DEV)
+    for seed, start in ((5, 0.0), (6, 1.0)):
+        q, k, v, g, beta = [t.clone() for t in base.make(T, H, H, dk, dv, True, seed)]
+        r = torch.Generator(device=DEV).manual_seed(seed)
+        g[w:] = -rate * torch.rand(T - w, H, dk, generator=r, device=DEV)
+        beta[w:] = 0.0
+        st = start * base.pool(1, H, dk, dv, seed)
+        s0 = base.np64(st[0])
+        f.prefill(q, k, v, g, beta, st, cu)
+        assert f.status() == lm.LING_MOE_OK
+        x = base.sub((q, k, v, g, beta), slice(0, T))
+        _, states = D.rule(*x, s0, dk**-0.5)
+        _, e = D.prefill_bound(*[t[:w] for t in x], s0, dk**-0.5)
+        left = np.exp(x[3][w:].sum(0)).max(-1)[:, None]      # [H, 1]: the channel that decays least
+        written = np.abs(np.stack([states[0] - np.exp(x[3][0])[..., None] * s0]
+                                  + [states[t] - np.exp(x[3][t])[..., None] * states[t - 1] for t in range(1, w)]))
+        tol = left * (e + (2.0**-22 + 720 * D.U + 2.0**-38 * dk) * (np.linalg.norm(written, axis=-2).sum(0)
+                                                                    + np.linalg.norm(s0, axis=-2)))
+        size = np.linalg.norm(states[-1], axis=-2)
+        assert np.linalg.norm(tol) < 0.05 * np.linalg.norm(size), "the bound says little"
+        worst = base.close_state(base.np64(st[0]), states[-1], tol)
+        rel = np.linalg.norm(base.np64(st[0]) - states[-1]) / np.linalg.norm(states[-1])
+        print(f"start {start}: {worst:.4f} of the bound, relative error {rel:.1e}, state {size.max():.1e}")
+    f.close()

@@ -519,10 +519,10 @@ struct PrepCfg {
   static constexpr int oB = oBefore + 8 * DK * 4, oInfo = oB + 256;
   // the slowest channel's decays: each token's, their products from the start of its 8-row block
   // and behind it to the end, the blocks' whole; the same from the start of its 16-row
-  // block, beta over that, and the powers of two of k's blocks
+  // block, beta over that, and the powers of two of k's rows
   static constexpr int oE = oInfo + 32, oEp = oE + 256, oEs = oEp + 256, oP = oEs + 256, oBp = oP + 256;
   static constexpr int oEt = oBp + 256, oPk = oEt + 32;
-  static constexpr int kSmem = oPk + 32;
+  static constexpr int kSmem = oPk + 256;
   // once the products are done: A and B in place of k s, v in place of q p, then
   // A's blocks below the diagonal and the inverses on it as fp16 in place of B
   static constexpr int oA = oKs, oBm = oKs + kMat, oV = oQ, oA16 = oBm;
@@ -938,14 +938,6 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
         if (w > warp) after[c] *= t;
       }
     store_row(sbefore + warp * DK + c0, before);
-    // k's operand is scaled by what its block decays to the end at least
-    float sk, ik, mk = 0.f;
-#pragma unroll
-    for (int c = 0; c < CPL; ++c) mk = fmaxf(mk, after[c]);
-    block_scale(warp_max_abs(mk), sk, ik);
-    if (lane == 0) spk[warp] = ik * kTopScale;
-#pragma unroll
-    for (int c = 0; c < CPL; ++c) after[c] *= sk;
     float x[CPL], first[CPL];
 #pragma unroll
     for (int c = 0; c < CPL; ++c) {
@@ -968,9 +960,15 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
       }
       store_half(dsm + C::oQ + r * C::kHRow + 2 * c0, qp, kOpScale);
       store_half(rec + 2 * KT + at, qt, kOpScale);
+      // k's row is scaled by its largest value: what the channels decay beyond the slowest adds up
+      float sk, ik, mk = 0.f;
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) mk = fmaxf(mk, fabsf(kh[c]));
+      block_scale(warp_max_abs(mk), sk, ik);
+      if (lane == 0) spk[r] = ik * kTopScale;
       uint32_t hi[CPL / 2], lo[CPL / 2];
 #pragma unroll
-      for (int c = 0; c < CPL / 2; ++c) split2(kh[2 * c], kh[2 * c + 1], hi[c], lo[c]);
+      for (int c = 0; c < CPL / 2; ++c) split2(kh[2 * c] * sk, kh[2 * c + 1] * sk, hi[c], lo[c]);
       if constexpr (CPL == 4) {
         *reinterpret_cast<uint2*>(rec + 3 * KT + at) = make_uint2(hi[0], hi[1]);
         *reinterpret_cast<uint2*>(rec + 4 * KT + at) = make_uint2(lo[0], lo[1]);
@@ -999,7 +997,7 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
       sP[tid] = x;
       sBp[tid] = sbeta[tid] / x;
       f[DK + tid] = x * up;
-      f[DK + 64 + tid] = sEs[tid] * down * spk[w];
+      f[DK + 64 + tid] = sEs[tid] * down * spk[tid];
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) all *= sEt[i];
