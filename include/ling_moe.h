@@ -450,7 +450,7 @@ int ling_moe_fp8_linear_test_set_wait(ling_moe_fp8_linear_t *h, int skip_cta, ui
 typedef struct {
   int k_heads, v_heads;  /* v_heads a multiple of k_heads */
   int head_k, head_v;    /* 64 or 128 each */
-  int max_tokens;        /* of a prefill call, all sequences together */
+  int max_tokens;        /* of a prefill call, all sequences together; steps need none of it: 1 will do for them alone */
   int max_seqs;          /* sequences of a call */
   float scale;           /* of the output; 0: 1 / sqrt(head_k) */
 } ling_moe_delta_config_t;

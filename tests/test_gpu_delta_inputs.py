@@ -73,6 +73,19 @@ def test_another_scale(scale):
     f.close()
 
 
+def test_a_handle_that_only_steps():
+    """max_tokens sizes the prefill alone: 1 is enough for windows of many sequences."""
+    H, d, B, n = 32, 128, 20, 8
+    small, large = lm.GatedDeltaRule(H, H, d, d, 1, B), lm.GatedDeltaRule(H, H, d, d, 500, B)
+    a = [t.view(B, n, *t.shape[1:]) for t in base.make(B * n, H, H, d, d, True, 85)]
+    s1 = base.pool(B, H, d, d, 85)
+    s2 = s1.clone()
+    assert torch.equal(small.step(*a, s1), large.step(*a, s2)) and torch.equal(s1, s2)
+    with pytest.raises(lm.LingMoEError):
+        small.prefill(*[t[0] for t in a], s1, i32([0, n]))
+    small.close(), large.close()
+
+
 def test_on_another_stream():
     """stream= as a torch stream and as its raw handle, while another one is current; outputs given and allocated."""
     T, H, d = 100, 4, 128

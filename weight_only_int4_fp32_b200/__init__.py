@@ -722,7 +722,8 @@ class GatedDeltaRule(_Handle):
     that `step` (decode and verify windows) and `prefill` (packed prompts) update in place.
     q and k are normalised inside; g are log-decays (<= 0), per channel [..., v_heads, head_k]
     or per head [..., v_heads]; beta are the write strengths.  scale: of the output
-    (None: head_k ** -0.5)."""
+    (None: head_k ** -0.5).  max_tokens: of a prefill call, which sizes its workspace (1
+    for a handle that only steps); max_seqs: of any call."""
 
     _destroy = "ling_moe_delta_destroy"
     MAX_STEP = 8

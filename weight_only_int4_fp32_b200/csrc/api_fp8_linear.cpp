@@ -135,7 +135,9 @@ int ling_moe_fp8_linear_forward(ling_moe_fp8_linear_t* h, const void* x, int64_t
   } else {
     // The tile width whose waves of tiles cost least.  A wave's time at K = 2560 is
     // 9.0, 10.2, 12.5 and 17.5 us for widths 32, 64, 128 and 256: a fixed part worth
-    // some 200 columns, and the width.
+    // some 200 columns, and the width.  Over 16 to 8192 tokens at 2560 x 1024, 2560 x 2560,
+    // 8192 x 2560, 8192 x 4096 and 2560 x 8192 (outputs x inputs) it takes the quickest of
+    // the four widths, or one within 6 % of it.
     p.tiles_m = (T + kF8TileM - 1) / kF8TileM;
     int tile = 0;
     long long best = 0;

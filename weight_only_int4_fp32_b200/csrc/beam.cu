@@ -27,9 +27,12 @@
 // sums and merges their sorted lists (a lane per segment), then one warp merges
 // the rows (a lane per row).
 //
-// Bound: issue slots of max and exp for large batches (224 live rows x 157184
-// bf16: 30 us, 70 MB at 2.3 TB/s; 55 us with candidates collected tile by tile),
-// latency (one or two tiles, two merges) for one request (9 us).  The segments depend on the call's sizes alone, not on
+// Bound: latency.  Large batches (224 live rows x 157184 bf16: 30 us, 70 MB at 2.3
+// TB/s; 55 us with candidates collected tile by tile) wait for their loads most (5.2
+// cycles per instruction; 68 % of the busiest scheduler's slots are used): an SM holds
+// three or four CTAs with one tile on its way each, and at 64 registers a thread of the
+// bf16 kernel spills 192 bytes.  One request (9 us) is one or two tiles and two
+// merges.  The segments depend on the call's sizes alone, not on
 // alignment, so equal rows give equal sums to the last bit.
 #include "beam.h"
 #include "common.cuh"

@@ -7,7 +7,7 @@
 //   o_t = scale * S^T q_t.
 //
 // Step (1..8 tokens per sequence): delta_step_kernel, the recurrence as it
-// stands with the state in registers.  HBM bound: the state read and written once.
+// stands with the state in registers: the state read and written once.
 //
 // Prefill: chunks of 64 tokens.  With G the running sum of g inside a chunk,
 //   A[i,j] = b_i sum_c k_i k_j exp(G_i - G_j)  (j < i),
@@ -250,10 +250,11 @@ __device__ __forceinline__ float transpose_sum32(float v[32]) {
 // S^T q + (k . q) u.  The warps of a CTA share the tokens' unit keys and
 // queries and their decays, which a warp per token prepares while the state is
 // on its way from HBM.
-// HBM bound for many heads: 64 sequences x 4 tokens, 32 heads of 128 x 128, 65 us,
-// 268 MB of states at 4.1 TB/s (32 columns per CTA with an exchange between its
-// warps per token: 89 us; without packed arithmetic and the next head's state on
-// its way: 86).  One sequence, one token: 4.3 us on the device.
+// Many heads: 64 sequences x 4 tokens, 32 heads of 128 x 128, 65 us, 268 MB of states
+// at 4.1 TB/s (32 columns per CTA with an exchange between its warps per token: 89 us;
+// without packed arithmetic and the next head's state on its way: 86).  DRAM is at 42 %
+// of its peak: a CTA's load, dependent tokens and stores follow one another,
+// and two CTAs per SM do not fill the gaps.  One sequence, one token: 4.4 us on the device.
 constexpr int kStepCols = 16;  // state columns of a warp
 // the place of channel c among a token's channels: R of them per row group, padded so
 // that the eight row groups' 16-byte reads fall into different banks
@@ -499,9 +500,10 @@ __global__ void __launch_bounds__(256, 2) delta_step_kernel(const DeltaParams p)
 // it.  W, q and k without the slowest decays.  fp16 rows have their 16-byte pieces
 // exchanged, piece ^= row % 8, for conflict-free ldmatrix.
 //
-// 56 us for 576 records of 128 x 128 heads (81 KB read, 123 KB written each): two
-// CTAs per SM (shared memory, 128 registers), whose own loads and dependent
-// phases are what the time goes to, not a rate.
+// 114 us for 1024 records of 128 x 128 heads (81 KB read, 124 KB written each): two
+// CTAs per SM (shared memory; 128 registers, 200 bytes a thread spilled), whose own
+// loads, dependent phases and instruction fetches (a long program, once per CTA) are
+// what the time goes to, not a rate.  What keeps the precision of decayed writes is 16 us of it.
 template <int DK>
 struct PrepCfg {
   static constexpr int kFRow = DK + 8;            // floats of a row of k p or k s
@@ -1218,9 +1220,9 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
 // operands through shared memory, with a barrier of the two each.  Operands are
 // two fp16 terms, a power of two per state column and half.  One more warp
 // brings the records, two ahead, by bulk copies.
-// A chunk takes 4200 cycles, 1.9 k of them mma.sync issue on each of the four
-// schedulers (18 chunks x 32 heads: 45 us); with a barrier of the whole CTA after
-// each of three products, and the inverse applied here, it took 7500.
+// A chunk takes 2.4 us (32 chunks x 32 heads: 76 us alone), mma.sync at 56 % of its rate
+// on each of the four schedulers; with a barrier of the whole CTA after each of three
+// products, and the inverse applied here, it took 4.5.
 constexpr int kScanTiles = 2;  // 16-column tiles per CTA
 
 template <int DK>
@@ -1231,7 +1233,7 @@ struct ScanCfg {
   static constexpr int kOps = delta_ops_bytes(DK);
   static constexpr int kKs = DK / 32;                      // 16-channel steps of a half
   static constexpr int kXS = 2 * kKs * 2 * 512;            // a column tile's S^T operand: halves, steps, terms
-  static constexpr int kXU = 2 * 2 * 3 * 512;              // its U^T operands: decayed to the chunk's end, two terms; as it is, one
+  static constexpr int kXU = 2 * 2 * 3 * 512;              // its U^T operands: to the chunk's end, two terms; as it is, one
   static constexpr int oX = 2 * kOps, oU = oX + MT * kXS;
   static constexpr int oFs = oU + MT * kXU, oFu = oFs + MT * 2 * 16 * 4;  // inverse scales [MT][half][16]
   static constexpr int oFb = oFu + MT * 2 * 16 * 4;

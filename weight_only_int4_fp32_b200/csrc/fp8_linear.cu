@@ -16,7 +16,7 @@
 //    fragments (e4m3 -> fp16 exactly), 16 outputs at a time per CTA, the blocks
 //    of K dealt to its 8 warps, tokens quantised in the same launch.  Bound:
 //    HBM, N x K bytes; at sizes of one projection, latency (2560 x 2560, one
-//    token: 5.5 us on the device; 8192 x 2560, eight: 11.4 us, 8 of them without
+//    token: 5.4 us on the device; 8192 x 2560, eight: 11.4 us, some 8 of them without
 //    the quantisation).
 //  * more: tcgen05 (kind::f8f6f4) tiles of 128 tokens x 32..256 outputs.  Each
 //    128-wide K block is one pipeline stage and one chain of four MMAs into
@@ -24,8 +24,9 @@
 //    add it to accumulators in registers while the next block multiplies.
 //    A quantisation kernel runs first, the tiles as its programmatic dependent.
 //    Bound: the way of a buffer between MMAs and promotion, and filling 48 KB
-//    per block, for many tokens (8192 x 8192 x 4096: 390 us, 1.4 PFLOP/s); HBM
-//    or one tile's K loop for few.
+//    per block, for many tokens (8192 x 8192 x 4096: 387 us, 1.42 PFLOP/s, in a row of
+//    ten; 357 in the best burst, 411 call after call, by the card's power); HBM or one
+//    tile's K loop for few (2560 x 2560: 13 us for 16 tokens, 15 for 256).
 // Source of the format: vLLM recipe page "inclusionAI/Ling-3.0-flash", section
 // Overview (the block-FP8 checkpoint); the page does not define it, the
 // definition above is this library's.
@@ -452,8 +453,9 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, float* v) {
 
 // The order of the tiles: bands of kF8Band token tiles, inside a band the token
 // tile fastest, so that the CTAs at work at one time share both their tokens
-// and their weights.  8192 x 8192 x 4096: 400 us with bands of 8 (4, 16, 32:
-// 413, 418, 415), 450 us with all token tiles in one.
+// and their weights.  Bands of 4, 8 and 16 take the same time within the run's noise at 16 to
+// 8192 tokens x 2560 to 8192 outputs x 1024 to 8192 inputs (8192 x 8192 x 4096: 356, 357
+// and 355 us); all token tiles in one band took an eighth longer.
 constexpr int kF8Band = 8;
 __device__ __forceinline__ void tile_place(const F8Params& p, int tile, int& m, int& n) {
   const int per = kF8Band * p.tiles_n, band = tile / per, in = tile - band * per;
@@ -466,7 +468,7 @@ __device__ __forceinline__ void tile_place(const F8Params& p, int tile, int& m, 
 // warp 16 issues the TMA loads, warp 17 the MMAs.  Every role walks the tiles
 // blockIdx.x, + gridDim.x, ...
 // (256 x 256 tiles over the two CTAs of a cluster, which read a third less, were
-// slower: 396 us in place of 375 for 8192 x 8192 x 4096.  A buffer's way from the
+// slower by a twentieth, in one run, at 8192 x 8192 x 4096.  A buffer's way from the
 // MMAs to the promotion and back takes longer between two CTAs, and it is what
 // bounds the loop.)
 template <int BN>
@@ -680,7 +682,9 @@ cudaError_t launch_f8_gemv(const F8Params& p, int sms, bool fused, cudaStream_t 
   if (!fused) return launch_dependent(f8_gemv_kernel<false>, grid, kGemvWarps * 32, 0, s, p);
   // Two CTAs share the quantisation where one alone would take more than a round
   // or two of loads: 8 tokens x 2560 inputs, 8192 outputs, 11.4 us (alone 14.5, four
-  // 12.2, eight 12.6).
+  // 12.2, eight 12.6).  Over 1 to 8 tokens x 1024 to 8192 inputs that is the quicker choice or
+  // within 0.5 us of it, but for exactly 64 pairs: one token x 8192 inputs takes 10.5 us
+  // alone and 8.8 shared, two x 4096 11.4 and 9.2.
   const int cluster = p.T * p.kb > 64 && grid >= 2 ? 2 : 1;
   grid = (grid + cluster - 1) / cluster * cluster;
   cudaLaunchConfig_t c{};
