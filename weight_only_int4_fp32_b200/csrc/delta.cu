@@ -46,6 +46,7 @@ constexpr float kOpScale = 1024.f;  // operands that are 2 at most are stored ti
 // A 16-row block's slowest decays in all, below which U~ is solved for without dividing by them:
 // of what is split after that division, the first rows keep 2^-38 / 2^-16 of the last ones.
 constexpr float kSteep = 0x1p-16f;
+constexpr uint32_t kLargeV = (127 + 100) << 7;  // bf16 2^100: such values are not divided by a decay either
 constexpr float kTopScale = 8192.f;  // block_scale brings the largest value to 2^13 at least
 constexpr float kNormEps = 1e-6f;
 // A row whose sum of squares passes fp32 is taken times 2^-40, twice at most: 128 of the largest
@@ -1069,6 +1070,7 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
   }
   __syncthreads();  // the operands are read: the matrices and v take their place
   for (int i = tid; i < 2 * C::kMat / 16; i += 256) reinterpret_cast<float4*>(dsm + C::oA)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  uint32_t vmax = 0u;  // the largest |v| among this thread's, even and odd channels apart
   {
     uint32_t x[8][2];
 #pragma unroll
@@ -1085,9 +1087,10 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
     for (int n = 0; n < 8; ++n) {
       const int i = n * 256 + tid, r = i / (p.dv / 4), c = 4 * (i % (p.dv / 4));
       if (r < kDeltaChunk) *reinterpret_cast<uint2*>(dsm + C::oV + r * C::kVRow + 2 * c) = make_uint2(x[n][0], x[n][1]);
+      vmax = __vmaxu2(vmax, __vmaxu2(x[n][0] & 0x7FFF7FFFu, x[n][1] & 0x7FFF7FFFu));
     }
   }
-  __syncthreads();
+  const bool large = __syncthreads_or((vmax & 0xFFFFu) >= kLargeV || (vmax >> 16) >= kLargeV);
   constexpr float kUn = 1.f / (kOpScale * kOpScale);
   {  // B's slowest decays: from the column to its block's end, from there to the row
     float d0 = sP[16 * ta + gq] * kUn, d1 = sP[16 * ta + gq + 8] * kUn;
@@ -1183,9 +1186,9 @@ __global__ void __launch_bounds__(256, 2) delta_prep_kernel(const DeltaParams p)
   }
   __syncthreads();
 
-  // ---- where a block's decay is steep: the inverses times the decays between their tokens,
+  // ---- where a block's decay is steep, or values are too large to divide by it: the inverses times the decays between their tokens,
   // a row of a block and four of its columns per thread
-  const bool steep = fminf(fminf(sP[15], sP[31]), fminf(sP[47], sP[63])) < kSteep;
+  const bool steep = large || fminf(fminf(sP[15], sP[31]), fminf(sP[47], sP[63])) < kSteep;
   if (steep) {
     const int r = tid >> 2, c0 = (r & 48) + 4 * (tid & 3);
     float d = 0.f;
